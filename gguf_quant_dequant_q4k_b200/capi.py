@@ -24,12 +24,17 @@ Q4K_ERR_RANGE = 7
 Q4K_ERR_CAPACITY = 8
 Q4K_FAULT_COPY_TIMEOUT = 1
 Q4K_FAULT_TOKEN_RANGE = 2
+Q4K_FAULT_ROUTE_RANGE = 4
 Q4K_QK = 256
 Q4K_BLOCK_BYTES = 144
 Q4K_MAX_M = 64
 Q4K_GEMV_X_READY = 0x1   # q4k_gemv_ex flag: x not written by the pending work on the stream
 Q4K_GEMM_K_MULTIPLE = 64
 Q4K_PREFILL_NOALLOC_MAX_ELEMS = 8388608
+Q4K_MOE_MAX_EXPERTS = 256
+Q4K_MOE_MAX_TOP_K = 16
+Q4K_MOE_GEMV_MAX_PAIRS = 4096
+Q4K_MOE_RENORM = 0x1     # q4k_moe_route flag: weights sum to 1 over the chosen experts
 Q4K_KERNEL_WARP_ROWS = 1
 Q4K_KERNEL_STREAM = 2
 Q4K_KERNEL_TC = 3
@@ -40,7 +45,9 @@ EXPORTS = ("q4k_gemv", "q4k_gemv_ex", "q4k_dequant_f32", "q4k_weight_bytes", "q4
            "q4k_last_cuda_error", "q4k_gemv_plan_for", "q4k_device_fault_flags",
            "q4k_embed_lookup_f32", "q4k_embed_gather_f32", "q4k_gemv_swiglu",
            "q4k_gemv_swiglu_plan_for", "q4k_selftest_wait_timeout", "q4k_dequant_f16",
-           "q4k_f32_to_f16", "q4k_gemm_f16", "q4k_prefill_f16", "q4k_prefill_f16_noalloc")
+           "q4k_f32_to_f16", "q4k_gemm_f16", "q4k_prefill_f16", "q4k_prefill_f16_noalloc",
+           "q4k_moe_route", "q4k_moe_gemv", "q4k_moe_gemv_swiglu", "q4k_moe_gemm_f16",
+           "q4k_moe_gemm_swiglu_f16", "q4k_moe_combine")
 
 
 class Q4KError(RuntimeError):
@@ -114,6 +121,17 @@ _lib.q4k_prefill_f16.restype = ctypes.c_int
 _lib.q4k_prefill_f16_noalloc.argtypes = [_vp, _vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          _vp]
 _lib.q4k_prefill_f16_noalloc.restype = ctypes.c_int
+_ci = ctypes.c_int
+_lib.q4k_moe_route.argtypes = [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, ctypes.c_uint, _vp]
+_lib.q4k_moe_route.restype = _ci
+for _name in ("q4k_moe_gemv", "q4k_moe_gemm_f16"):
+    getattr(_lib, _name).argtypes = [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp]
+    getattr(_lib, _name).restype = _ci
+for _name in ("q4k_moe_gemv_swiglu", "q4k_moe_gemm_swiglu_f16"):
+    getattr(_lib, _name).argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _ci, _ci, _vp]
+    getattr(_lib, _name).restype = _ci
+_lib.q4k_moe_combine.argtypes = [_vp, _vp, _vp, _vp, _vp, _ci, _ci, _ci, _vp]
+_lib.q4k_moe_combine.restype = _ci
 
 
 def library() -> ctypes.CDLL:
@@ -397,3 +415,129 @@ def q4k_prefill_f16_noalloc(w16, x, y, m: int, n: int, k: int, stream=None) -> N
     st = q4k_prefill_f16_noalloc_status(w16, x, y, m, n, k, stream)
     if st != Q4K_OK:
         raise Q4KError(st, "q4k_prefill_f16_noalloc")
+
+
+# --------------------------------------------------------------------------- mixture of experts
+
+def q4k_moe_route_status(logits, ids, weights, offsets, order, n_tokens: int, n_experts: int,
+                         top_k: int, renorm: bool = True, stream=None) -> int:
+    """Raw status of the C call (no exception; tensor checks still raise)."""
+    ok = (n_tokens >= 0 and 1 <= n_experts <= Q4K_MOE_MAX_EXPERTS
+          and 1 <= top_k <= min(n_experts, Q4K_MOE_MAX_TOP_K))
+    pairs = _need(n_tokens * top_k, 4, ok)
+    return _lib.q4k_moe_route(_ptr(logits, "float32", "logits", _need(n_tokens * n_experts, 4, ok)),
+                              _ptr(ids, "int32", "ids", pairs),
+                              _ptr(weights, "float32", "weights", pairs),
+                              _ptr(offsets, "int32", "offsets", _need(n_experts + 1, 4, ok)),
+                              _ptr(order, "int32", "order", pairs), int(n_tokens), int(n_experts),
+                              int(top_k), Q4K_MOE_RENORM if renorm else 0, _stream(stream))
+
+
+def q4k_moe_route(logits, ids, weights, offsets, order, n_tokens: int, n_experts: int, top_k: int,
+                  renorm: bool = True, stream=None) -> None:
+    """ids, weights [n_tokens, top_k]: the experts of largest logits[n_tokens, n_experts] and their
+    softmax weights (renorm: over the chosen ones, else over all); offsets [n_experts + 1] and
+    order [n_tokens * top_k]: the pairs grouped by expert."""
+    st = q4k_moe_route_status(logits, ids, weights, offsets, order, n_tokens, n_experts, top_k,
+                              renorm, stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_route")
+
+
+def _moe_product(fn, ws, x, xtype: str, offsets, order, y, ytype: str, max_pairs: int | None,
+                 n_experts: int, n_pairs: int, pairs_per_row: int, n: int, k: int, stream) -> int:
+    ok = (q4k_weight_bytes(n, k) > 0 and 1 <= n_experts <= Q4K_MOE_MAX_EXPERTS and n_pairs > 0
+          and pairs_per_row >= 0 and (max_pairs is None or n_pairs <= max_pairs))
+    rows = n_pairs if pairs_per_row <= 0 else -(-n_pairs // pairs_per_row)
+    wb = _need(n_experts * q4k_weight_bytes(n, k), 1, ok)
+    item = {"float32": 4, "float16": 2}
+    return fn(*(_ptr(w, None, name, wb) for name, w in ws),
+              _ptr(x, xtype, "x", _need(rows * k, item[xtype], ok)),
+              _ptr(offsets, "int32", "offsets", _need(n_experts + 1, 4, ok)),
+              _ptr(order, "int32", "order", _need(n_pairs, 4, ok)),
+              _ptr(y, ytype, "y", _need(n_pairs * n, item[ytype], ok)), int(n_experts), int(n_pairs),
+              int(pairs_per_row), int(n), int(k), _stream(stream))
+
+
+def q4k_moe_gemv_status(w, x, offsets, order, y, n_experts: int, n_pairs: int, pairs_per_row: int,
+                        n: int, k: int, stream=None) -> int:
+    return _moe_product(_lib.q4k_moe_gemv, (("w", w),), x, "float32", offsets, order, y, "float32",
+                        Q4K_MOE_GEMV_MAX_PAIRS, n_experts, n_pairs, pairs_per_row, n, k, stream)
+
+
+def q4k_moe_gemv(w, x, offsets, order, y, n_experts: int, n_pairs: int, pairs_per_row: int, n: int,
+                 k: int, stream=None) -> None:
+    """y[order[s], n] = W_e[n, k] x[row(s), k] for every slot s of every expert e; x rows by slot
+    (pairs_per_row 0) or by order[s] // pairs_per_row."""
+    st = q4k_moe_gemv_status(w, x, offsets, order, y, n_experts, n_pairs, pairs_per_row, n, k, stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_gemv")
+
+
+def q4k_moe_gemv_swiglu_status(w_gate, w_up, x, offsets, order, h, n_experts: int, n_pairs: int,
+                               pairs_per_row: int, n: int, k: int, stream=None) -> int:
+    return _moe_product(_lib.q4k_moe_gemv_swiglu, (("w_gate", w_gate), ("w_up", w_up)), x, "float32",
+                        offsets, order, h, "float32", Q4K_MOE_GEMV_MAX_PAIRS, n_experts, n_pairs,
+                        pairs_per_row, n, k, stream)
+
+
+def q4k_moe_gemv_swiglu(w_gate, w_up, x, offsets, order, h, n_experts: int, n_pairs: int,
+                        pairs_per_row: int, n: int, k: int, stream=None) -> None:
+    """h[s, n] = silu(Wg_e x[row(s)]) * (Wu_e x[row(s)]), rows in slot order."""
+    st = q4k_moe_gemv_swiglu_status(w_gate, w_up, x, offsets, order, h, n_experts, n_pairs,
+                                    pairs_per_row, n, k, stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_gemv_swiglu")
+
+
+def q4k_moe_gemm_f16_status(w, x16, offsets, order, y, n_experts: int, n_pairs: int,
+                            pairs_per_row: int, n: int, k: int, stream=None) -> int:
+    return _moe_product(_lib.q4k_moe_gemm_f16, (("w", w),), x16, "float16", offsets, order, y,
+                        "float32", None, n_experts, n_pairs, pairs_per_row, n, k, stream)
+
+
+def q4k_moe_gemm_f16(w, x16, offsets, order, y, n_experts: int, n_pairs: int, pairs_per_row: int,
+                     n: int, k: int, stream=None) -> None:
+    """y[order[s], n] = x16[row(s), k] @ W16_e[n, k]^T (W16_e: the fp16 mirror's values, formed in
+    the kernel from the Q4_K matrix)."""
+    st = q4k_moe_gemm_f16_status(w, x16, offsets, order, y, n_experts, n_pairs, pairs_per_row, n, k,
+                                 stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_gemm_f16")
+
+
+def q4k_moe_gemm_swiglu_f16_status(w_gate, w_up, x16, offsets, order, h16, n_experts: int,
+                                   n_pairs: int, pairs_per_row: int, n: int, k: int,
+                                   stream=None) -> int:
+    return _moe_product(_lib.q4k_moe_gemm_swiglu_f16, (("w_gate", w_gate), ("w_up", w_up)), x16,
+                        "float16", offsets, order, h16, "float16", None, n_experts, n_pairs,
+                        pairs_per_row, n, k, stream)
+
+
+def q4k_moe_gemm_swiglu_f16(w_gate, w_up, x16, offsets, order, h16, n_experts: int, n_pairs: int,
+                            pairs_per_row: int, n: int, k: int, stream=None) -> None:
+    """h16[s, n] (float16) = silu(g) * u of the fp16 products g, u, rows in slot order."""
+    st = q4k_moe_gemm_swiglu_f16_status(w_gate, w_up, x16, offsets, order, h16, n_experts, n_pairs,
+                                        pairs_per_row, n, k, stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_gemm_swiglu_f16")
+
+
+def q4k_moe_combine_status(z, ids, weights, residual, y, n_tokens: int, top_k: int, hidden: int,
+                           stream=None) -> int:
+    ok = n_tokens > 0 and hidden > 0 and 1 <= top_k <= Q4K_MOE_MAX_TOP_K
+    rows, pairs = _need(n_tokens * hidden, 4, ok), _need(n_tokens * top_k, 4, ok)
+    return _lib.q4k_moe_combine(_ptr(z, "float32", "z", rows * top_k if ok else 0),
+                                _ptr(ids, "int32", "ids", pairs),
+                                _ptr(weights, "float32", "weights", pairs),
+                                _ptr(residual, "float32", "residual", rows),
+                                _ptr(y, "float32", "y", rows), int(n_tokens), int(top_k), int(hidden),
+                                _stream(stream))
+
+
+def q4k_moe_combine(z, ids, weights, residual, y, n_tokens: int, top_k: int, hidden: int,
+                    stream=None) -> None:
+    """y[t] = residual[t] (or 0) + sum_j weights[t, j] * z[t * top_k + j], j with ids[t, j] >= 0."""
+    st = q4k_moe_combine_status(z, ids, weights, residual, y, n_tokens, top_k, hidden, stream)
+    if st != Q4K_OK:
+        raise Q4KError(st, "q4k_moe_combine")

@@ -20,6 +20,7 @@
 #include "q4k_gemv_i8.h"
 #include "q4k_gemv_tc.h"
 #include "q4k_internal.h"
+#include "q4k_moe.h"
 #include "q4k_stream.h"
 
 namespace q4k {
@@ -76,6 +77,10 @@ int current_device_info(DeviceInfo* info) {
             g_dev_status[dev] = q4k_last_cuda_error_value();
         if (g_dev_status[dev] == 0 && i8_set_attributes() != Q4K_OK)
             g_dev_status[dev] = q4k_last_cuda_error_value();
+        if (g_dev_status[dev] == 0 && moe_gemv_set_attributes() != Q4K_OK)
+            g_dev_status[dev] = q4k_last_cuda_error_value();
+        if (g_dev_status[dev] == 0 && moe_gemm_set_attributes() != Q4K_OK)
+            g_dev_status[dev] = q4k_last_cuda_error_value();
         if (g_dev_status[dev] == 0) {
             stream_cluster_occupancy(1, g_dev[dev].max_clusters[0]);
             stream_cluster_occupancy(2, g_dev[dev].max_clusters[1]);
@@ -115,7 +120,7 @@ int q4k_last_cuda_error(void) { return t_last_cuda_error; }
 
 int q4k_device_fault_flags(unsigned int* flags) {
     if (flags == nullptr) return Q4K_ERR_NULL;
-    unsigned a = 0, b = 0, c = 0, t = 0, i = 0;
+    unsigned a = 0, b = 0, c = 0, t = 0, i = 0, mv = 0, mm = 0;
     int st = read_fault_flags(&a);
     if (st != Q4K_OK) return st;
     st = read_embed_fault_flags(&b);
@@ -126,7 +131,11 @@ int q4k_device_fault_flags(unsigned int* flags) {
     if (st != Q4K_OK) return st;
     st = read_i8_fault_flags(&i);
     if (st != Q4K_OK) return st;
-    *flags = a | b | c | t | i;
+    st = read_moe_gemv_fault_flags(&mv);
+    if (st != Q4K_OK) return st;
+    st = read_moe_gemm_fault_flags(&mm);
+    if (st != Q4K_OK) return st;
+    *flags = a | b | c | t | i | mv | mm;
     return Q4K_OK;
 }
 
@@ -345,6 +354,137 @@ int q4k_prefill_f16_noalloc(const void* w_f16, const float* x, float* y, int m, 
     if (e != cudaSuccess) return cuda_failure(e);
     return launch_prefill_noalloc(device, w_f16, x, y, m, n, k, dev.sm_count,
                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- mixture of experts
+
+int q4k_moe_route(const float* logits, int* ids, float* weights, int* offsets, int* order, int n_tokens,
+                  int n_experts, int top_k, unsigned flags, q4k_stream_t stream) {
+    if (offsets == nullptr) return Q4K_ERR_NULL;
+    if (n_tokens > 0 && (logits == nullptr || ids == nullptr || weights == nullptr || order == nullptr))
+        return Q4K_ERR_NULL;
+    if (n_tokens < 0 || n_experts < 1 || n_experts > Q4K_MOE_MAX_EXPERTS || top_k < 1 || top_k > n_experts ||
+        top_k > Q4K_MOE_MAX_TOP_K || (flags & ~Q4K_MOE_RENORM) != 0u ||
+        static_cast<long long>(n_tokens) * top_k > INT32_MAX)
+        return Q4K_ERR_SHAPE;
+    if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(order, 4))
+        return Q4K_ERR_ALIGN;
+    const size_t lbytes = static_cast<size_t>(n_tokens) * static_cast<size_t>(n_experts) * 4;
+    const size_t pbytes = static_cast<size_t>(n_tokens) * static_cast<size_t>(top_k) * 4;
+    const size_t obytes = static_cast<size_t>(n_experts + 1) * 4;
+    if (n_tokens > 0) {
+        const void* out[4] = {ids, weights, order, offsets};
+        const size_t len[4] = {pbytes, pbytes, pbytes, obytes};
+        for (int i = 0; i < 4; ++i) {
+            if (overlaps(out[i], len[i], logits, lbytes)) return Q4K_ERR_OVERLAP;
+            for (int j = 0; j < i; ++j)
+                if (overlaps(out[i], len[i], out[j], len[j])) return Q4K_ERR_OVERLAP;
+        }
+    }
+    DeviceInfo dev;
+    int st = current_device_info(&dev);
+    if (st != Q4K_OK) return st;
+    return launch_moe_route(logits, ids, weights, offsets, order, n_tokens, n_experts, top_k,
+                            (flags & Q4K_MOE_RENORM) != 0u, dev.sm_count, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// Checks shared by the grouped products (x, y elements of xsize, ysize bytes;
+// w2 null for the plain forms), and the group description they launch with.
+int check_moe_product(const void* w, const void* w2, bool swiglu, const void* x, size_t xsize, const int* offsets,
+                      const int* order, const void* y, size_t ysize, uintptr_t yalign, int n_experts, int n_pairs,
+                      int per_row, int n, int k, int max_pairs, MoeGroups* g) {
+    if (w == nullptr || (swiglu && w2 == nullptr) || offsets == nullptr) return Q4K_ERR_NULL;
+    if (n_pairs > 0 && (x == nullptr || order == nullptr || y == nullptr)) return Q4K_ERR_NULL;
+    const size_t wexpert = weight_bytes_checked(n, k);
+    if (wexpert == 0 || n_experts < 1 || n_experts > Q4K_MOE_MAX_EXPERTS || n_pairs < 0 || per_row < 0 ||
+        static_cast<long long>(n_experts) * n > INT32_MAX)
+        return Q4K_ERR_SHAPE;
+    if (n_pairs > max_pairs) return Q4K_ERR_UNSUPPORTED_M;
+    if (!aligned(w, 16) || !aligned(w2, 16) || !aligned(x, 16) || !aligned(y, yalign) || !aligned(offsets, 4) ||
+        !aligned(order, 4))
+        return Q4K_ERR_ALIGN;
+    const int x_rows = per_row == 0 ? n_pairs : static_cast<int>((static_cast<long long>(n_pairs) + per_row - 1) / per_row);
+    const size_t wbytes = wexpert * static_cast<size_t>(n_experts);
+    const size_t xbytes = static_cast<size_t>(x_rows) * static_cast<size_t>(k) * xsize;
+    const size_t ybytes = static_cast<size_t>(n_pairs) * static_cast<size_t>(n) * ysize;
+    if (n_pairs > 0 &&
+        (overlaps(y, ybytes, w, wbytes) || (swiglu && overlaps(y, ybytes, w2, wbytes)) || overlaps(y, ybytes, x, xbytes) ||
+         overlaps(y, ybytes, offsets, static_cast<size_t>(n_experts + 1) * 4) ||
+         overlaps(y, ybytes, order, static_cast<size_t>(n_pairs) * 4)))
+        return Q4K_ERR_OVERLAP;
+    *g = MoeGroups{offsets, order, n_experts, n_pairs, per_row, x_rows};
+    return Q4K_OK;
+}
+
+int moe_gemv(const void* w, const void* w2, bool swiglu, const float* x, const int* offsets, const int* order, float* y,
+             int n_experts, int n_pairs, int per_row, int n, int k, q4k_stream_t stream) {
+    MoeGroups g;
+    int st = check_moe_product(w, w2, swiglu, x, 4, offsets, order, y, 4, 4, n_experts, n_pairs, per_row, n, k,
+                               Q4K_MOE_GEMV_MAX_PAIRS, &g);
+    if (st != Q4K_OK || n_pairs == 0) return st;
+    DeviceInfo dev;
+    st = current_device_info(&dev);
+    if (st != Q4K_OK) return st;
+    return launch_moe_gemv(dev, w, swiglu ? w2 : nullptr, x, g, y, n, k, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_gemm(const void* w, const void* w2, bool swiglu, const void* x, const int* offsets, const int* order, void* y,
+             int n_experts, int n_pairs, int per_row, int n, int k, q4k_stream_t stream) {
+    MoeGroups g;
+    int st = check_moe_product(w, w2, swiglu, x, 2, offsets, order, y, swiglu ? 2 : 4, swiglu ? 16 : 4, n_experts,
+                               n_pairs, per_row, n, k, INT32_MAX, &g);
+    if (st != Q4K_OK || n_pairs == 0) return st;
+    DeviceInfo dev;
+    st = current_device_info(&dev);
+    if (st != Q4K_OK) return st;
+    return launch_moe_gemm(dev, w, swiglu ? w2 : nullptr, x, g, y, n, k, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+int q4k_moe_gemv(const void* w, const float* x, const int* offsets, const int* order, float* y, int n_experts,
+                 int n_pairs, int pairs_per_row, int n, int k, q4k_stream_t stream) {
+    return moe_gemv(w, nullptr, false, x, offsets, order, y, n_experts, n_pairs, pairs_per_row, n, k, stream);
+}
+
+int q4k_moe_gemv_swiglu(const void* w_gate, const void* w_up, const float* x, const int* offsets, const int* order,
+                        float* h, int n_experts, int n_pairs, int pairs_per_row, int n, int k, q4k_stream_t stream) {
+    return moe_gemv(w_gate, w_up, true, x, offsets, order, h, n_experts, n_pairs, pairs_per_row, n, k, stream);
+}
+
+int q4k_moe_gemm_f16(const void* w, const void* x_f16, const int* offsets, const int* order, float* y, int n_experts,
+                     int n_pairs, int pairs_per_row, int n, int k, q4k_stream_t stream) {
+    return moe_gemm(w, nullptr, false, x_f16, offsets, order, y, n_experts, n_pairs, pairs_per_row, n, k, stream);
+}
+
+int q4k_moe_gemm_swiglu_f16(const void* w_gate, const void* w_up, const void* x_f16, const int* offsets,
+                            const int* order, void* h_f16, int n_experts, int n_pairs, int pairs_per_row, int n, int k,
+                            q4k_stream_t stream) {
+    return moe_gemm(w_gate, w_up, true, x_f16, offsets, order, h_f16, n_experts, n_pairs, pairs_per_row, n, k, stream);
+}
+
+int q4k_moe_combine(const float* z, const int* ids, const float* weights, const float* residual, float* y, int n_tokens,
+                    int top_k, int hidden, q4k_stream_t stream) {
+    if (n_tokens > 0 && (z == nullptr || ids == nullptr || weights == nullptr || y == nullptr)) return Q4K_ERR_NULL;
+    if (n_tokens < 0 || hidden <= 0 || hidden % 4 != 0 || top_k < 1 || top_k > Q4K_MOE_MAX_TOP_K ||
+        static_cast<long long>(n_tokens) * top_k > INT32_MAX)
+        return Q4K_ERR_SHAPE;
+    if (!aligned(z, 16) || !aligned(residual, 16) || !aligned(y, 16) || !aligned(ids, 4) || !aligned(weights, 4))
+        return Q4K_ERR_ALIGN;
+    if (n_tokens == 0) return Q4K_OK;
+    const size_t ybytes = static_cast<size_t>(n_tokens) * static_cast<size_t>(hidden) * 4;
+    const size_t pbytes = static_cast<size_t>(n_tokens) * static_cast<size_t>(top_k) * 4;
+    if (overlaps(y, ybytes, z, ybytes * static_cast<size_t>(top_k)) || overlaps(y, ybytes, ids, pbytes) ||
+        overlaps(y, ybytes, weights, pbytes) ||
+        (residual != nullptr && residual != y && overlaps(y, ybytes, residual, ybytes)))
+        return Q4K_ERR_OVERLAP;
+    DeviceInfo dev;
+    int st = current_device_info(&dev);
+    if (st != Q4K_OK) return st;
+    return launch_moe_combine(z, ids, weights, residual, y, n_tokens, top_k, hidden, dev.sm_count,
+                              reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -79,12 +79,17 @@ enum q4k_status {
 #define Q4K_FAULT_COPY_TIMEOUT 1u  /* a bounded wait on a bulk copy, a tensor copy or an
                                       MMA commit gave up                               */
 #define Q4K_FAULT_TOKEN_RANGE 2u   /* q4k_embed_gather_f32 met a token outside the table */
+#define Q4K_FAULT_ROUTE_RANGE 4u   /* a q4k_moe product met offsets or an order entry
+                                      outside the pairs                                */
 
 #define Q4K_QK 256          /* weights per superblock */
 #define Q4K_BLOCK_BYTES 144 /* bytes per superblock   */
 #define Q4K_MAX_M 64        /* most vectors per q4k_gemv call */
 #define Q4K_GEMM_K_MULTIPLE 64 /* q4k_gemm_f16 / q4k_prefill_f16: k % 64 == 0 */
 #define Q4K_PREFILL_NOALLOC_MAX_ELEMS 8388608 /* q4k_prefill_f16_noalloc: m*k limit (16 MiB fp16) */
+#define Q4K_MOE_MAX_EXPERTS 256 /* q4k_moe_*: most experts                       */
+#define Q4K_MOE_MAX_TOP_K 16    /* q4k_moe_route / q4k_moe_combine: most choices */
+#define Q4K_MOE_GEMV_MAX_PAIRS 4096 /* q4k_moe_gemv*: most pairs per call         */
 
 /*
  * y = W x for m vectors.
@@ -265,7 +270,9 @@ Q4K_API int q4k_embed_gather_f32(const void *table, unsigned long long table_byt
  * Q4K_FAULT_COPY_TIMEOUT if a bounded wait inside a kernel on a bulk copy into
  * shared memory gave up (the kernel then skipped its remaining work and
  * returned; its output is invalid; never happens in normal operation);
- * Q4K_FAULT_TOKEN_RANGE if q4k_embed_gather_f32 met a token outside its table.
+ * Q4K_FAULT_TOKEN_RANGE if q4k_embed_gather_f32 met a token outside its table;
+ * Q4K_FAULT_ROUTE_RANGE if a q4k_moe product met offsets or order entries
+ * outside its pairs.
  * Synchronises the device. Returns a q4k_status; *flags receives the flags.
  */
 Q4K_API int q4k_device_fault_flags(unsigned int *flags);
@@ -425,6 +432,120 @@ Q4K_API int q4k_prefill_f16(const void *w_f16, const float *x, void *x_f16_scrat
  */
 Q4K_API int q4k_prefill_f16_noalloc(const void *w_f16, const float *x, float *y, int m, int n,
                                     int k, q4k_stream_t stream);
+
+/*
+ * ---- Mixture of experts ----
+ * The feed-forward layer of a mixture-of-experts model around the Q4_K
+ * projections: the router (q4k_moe_route), the expert projections (single
+ * tokens: q4k_moe_gemv_swiglu, q4k_moe_gemv; prompts: q4k_moe_gemm_swiglu_f16,
+ * q4k_moe_gemm_f16) and the weighted sum (q4k_moe_combine). No reference page
+ * has these; they extend q4k_gemv, q4k_gemv_swiglu and q4k_gemm_f16 to a batch
+ * in which every token picks its own matrices.
+ *
+ * Pairs and slots. Pair p = t * top_k + j is token t's j-th choice. The routed
+ * pairs sorted by expert, and by p within an expert, fill slots 0, 1, ...:
+ * expert e owns slots offsets[e] .. offsets[e + 1] - 1 (offsets: n_experts + 1
+ * int32 from offsets[0] = 0) and order[s] (n_pairs int32) is the pair in slot
+ * s, -1 behind the last slot. A pair without an expert (ids -1) has no slot.
+ *
+ * Products read row per slot and expert: x row of slot s is s where
+ * pairs_per_row is 0 (rows in slot order), else order[s] / pairs_per_row
+ * (top_k: one row per token; 1: one row per pair). The SwiGLU forms write rows
+ * in slot order (what the down projection reads with pairs_per_row 0), the
+ * plain forms rows in pair order (what q4k_moe_combine reads). Rows of slots
+ * behind the last, and of pairs without an expert, are left as they were.
+ *   w (w_gate, w_up): n_experts consecutive N x K Q4_K matrices, each laid out
+ *        as w of q4k_gemv, 16-byte aligned.
+ *   x  : n_pairs rows (pairs_per_row 0), else ceil(n_pairs / pairs_per_row)
+ *        rows, of K elements, 16-byte aligned.
+ *   y  : n_pairs x N, row-major.
+ *   offsets, order: device memory, 4-byte aligned, as q4k_moe_route writes
+ *        them. They cannot be checked before launch: an expert whose offsets
+ *        do not ascend within 0..n_pairs, and a slot whose order entry lies
+ *        outside 0..n_pairs-1, is skipped (its rows unwritten) and raises
+ *        Q4K_FAULT_ROUTE_RANGE. Order entries must be distinct.
+ * n_experts 1..Q4K_MOE_MAX_EXPERTS (more: Q4K_ERR_SHAPE), n_experts * N below
+ * 2^31; n_pairs == 0 launches nothing. Outputs must not overlap inputs.
+ */
+
+/*
+ * The router: per token the top_k experts of largest logit, ties to the lower
+ * expert, in descending order, with softmax weights; and the grouping above.
+ *   logits : n_tokens x n_experts float32, 4-byte aligned. NaN and -inf mean
+ *            "not available" (never chosen, weight 0 in every sum); +inf counts
+ *            as the largest finite value.
+ *   ids    : n_tokens x top_k int32 (-1: no expert left for that choice).
+ *   weights: n_tokens x top_k float32: exp(l - max l) over the sum of the same
+ *            over the chosen experts (flags & Q4K_MOE_RENORM) or over all
+ *            available ones; 0 where ids is -1.
+ *   offsets: n_experts + 1 int32; order: n_tokens * top_k int32.
+ * top_k 1..min(n_experts, Q4K_MOE_MAX_TOP_K), n_tokens >= 0 (0: only offsets is
+ * written, the other pointers may be NULL), n_tokens * top_k below 2^31 (else
+ * Q4K_ERR_SHAPE; other bits of flags too). Results are bit-reproducible.
+ * Returns a q4k_status.
+ */
+#define Q4K_MOE_RENORM 0x1u
+Q4K_API int q4k_moe_route(const float *logits, int *ids, float *weights, int *offsets, int *order,
+                          int n_tokens, int n_experts, int top_k, unsigned flags,
+                          q4k_stream_t stream);
+
+/*
+ * y[order[s]] = W_e x[row(s)] for every slot s of every expert e, in f32
+ * (rows in pair order). n_pairs 0..Q4K_MOE_GEMV_MAX_PAIRS (more:
+ * Q4K_ERR_UNSUPPORTED_M: that is q4k_moe_gemm_f16's size). K a positive
+ * multiple of 256. y 4-byte aligned.
+ * Accuracy: as q4k_gemv for the same row and matrix.
+ * Returns a q4k_status.
+ */
+Q4K_API int q4k_moe_gemv(const void *w, const float *x, const int *offsets, const int *order,
+                         float *y, int n_experts, int n_pairs, int pairs_per_row, int n, int k,
+                         q4k_stream_t stream);
+
+/*
+ * h[s] = silu(Wg_e x[row(s)]) * (Wu_e x[row(s)]), rows in slot order.
+ * Sizes as q4k_moe_gemv; accuracy as q4k_gemv_swiglu.
+ * Returns a q4k_status.
+ */
+Q4K_API int q4k_moe_gemv_swiglu(const void *w_gate, const void *w_up, const float *x,
+                                const int *offsets, const int *order, float *h, int n_experts,
+                                int n_pairs, int pairs_per_row, int n, int k, q4k_stream_t stream);
+
+/*
+ * y[order[s]] = x16[row(s)] * W16_e^T for every slot s of every expert e: the
+ * products of q4k_gemm_f16 on the experts' fp16 mirrors, without a mirror in
+ * memory (W16_e: the values q4k_dequant_f16 gives, formed inside the kernel).
+ *   x_f16: binary16 rows (q4k_f32_to_f16); y: float32, 4-byte aligned, rows in
+ *   pair order.
+ * Accuracy: as q4k_gemm_f16. Returns a q4k_status.
+ */
+Q4K_API int q4k_moe_gemm_f16(const void *w, const void *x_f16, const int *offsets, const int *order,
+                             float *y, int n_experts, int n_pairs, int pairs_per_row, int n, int k,
+                             q4k_stream_t stream);
+
+/*
+ * h16[s] = binary16 of silu(g) * u, g = x16[row(s)] * Wg16_e^T and
+ * u = x16[row(s)] * Wu16_e^T, rows in slot order, 16-byte aligned: the x_f16
+ * of the down projection (pairs_per_row 0).
+ * Returns a q4k_status.
+ */
+Q4K_API int q4k_moe_gemm_swiglu_f16(const void *w_gate, const void *w_up, const void *x_f16,
+                                    const int *offsets, const int *order, void *h_f16,
+                                    int n_experts, int n_pairs, int pairs_per_row, int n, int k,
+                                    q4k_stream_t stream);
+
+/*
+ * y[t] = residual[t] + sum_j weights[t][j] * z[t * top_k + j], over the j with
+ * ids[t][j] >= 0, added in that order in f32 (residual NULL: from 0). Rows of z
+ * without an expert are not read.
+ *   z: n_tokens * top_k rows, residual, y: n_tokens rows of `hidden` float32,
+ *   16-byte aligned; hidden a positive multiple of 4; top_k
+ *   1..Q4K_MOE_MAX_TOP_K; ids, weights 4-byte aligned. y may be residual
+ *   itself; other overlaps of y are refused. n_tokens == 0 launches nothing.
+ * Returns a q4k_status.
+ */
+Q4K_API int q4k_moe_combine(const float *z, const int *ids, const float *weights,
+                            const float *residual, float *y, int n_tokens, int top_k, int hidden,
+                            q4k_stream_t stream);
 
 #ifdef __cplusplus
 }
