@@ -1,30 +1,615 @@
-// q4k_moe_gemm.cu -- Q4_K products grouped by expert (fp16 x, weights rounded to the fp16 mirror).
-#include "q4k_moe_rows.cuh"
+// q4k_moe_gemm.cu -- expert-grouped products of fp16 activations with Q4_K
+// matrices (q4k_moe_gemm_f16, q4k_moe_gemm_swiglu_f16): y = x16 * W16_e^T, W16
+// the fp16 mirror's values (the f32 weight d*sc*q - dmin*m rounded to
+// binary16), formed inside the kernel from the superblocks.
+//
+// * Tiles. A pair of CTAs (one cluster, tensor cores joined by cta_group::2)
+//   owns a tile of y^T: 256 rows of W_e (the MMA's M, 128 per CTA) by up to 192
+//   slots of expert e (N). An expert's slots are cut into equal blocks of at
+//   most 192; N is the block's slots rounded up to 16. SwiGLU: 128 gate and 128
+//   up rows, per CTA 64 and 64, so that TMEM lanes 32q + l and 32q + 16 + l
+//   (l < 16) hold gate and up of one feature. 74 persistent pairs walk the
+//   tiles of all experts, the blocks of a row tile one after another.
+// * A (weights). A producer streams 128 rows x 144 bytes per superblock into a
+//   shared-memory ring (TMA). Two sets of four decode warps (a warp per TMEM
+//   lane quarter, a lane per row) take alternate 64-weight groups: a nibble
+//   becomes the f32 16 + q by one byte permute, the weight one packed fma with
+//   (d*sc, -(dmin*m + 16*d*sc)), rounded once, then cvt to fp16 pairs, stored
+//   to TMEM. The folded constant is exact unless d and dmin are further apart
+//   than 2^10 (or 2^-2); such superblocks take q first (one more fma). The
+//   decoded group feeds all N slots, so decoding (about 750 of the SM's issue
+//   cycles per superblock) hides behind the MMAs for N >= 96 (8 N cycles).
+// * B (activations). 64 elements of N / 2 rows per CTA and step, fetched by row
+//   (TMA gather of four rows) or, for x in slot order, as tiles, in the
+//   128-byte-swizzled layout; the pair's tensor cores share the two halves.
+// * D. Two TMEM accumulators of 192 columns take turns: the epilogue empties
+//   one while the MMAs fill the other. The tensor core adds to D by truncation
+//   (measured 1.7e-5 relative over K = 14336); every kPlainChunk superblocks
+//   the plain form therefore moves D into f32 registers, rounding to nearest
+//   (under 1e-6). The SwiGLU form rounds to fp16 and keeps D for the whole row.
+// * Waits are bounded; a role that gives up raises Q4K_FAULT_COPY_TIMEOUT and
+//   the CTA lets its copies and MMAs land before shared memory and TMEM go.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "q4k_internal.h"
+#include "q4k_moe.h"
+#include "q4k_pair.cuh"
+#include "q4k_superblock.cuh"
+#include "q4k_swiglu.cuh"
 
 namespace q4k {
 
 __device__ unsigned int g_moe_gemm_fault_flags = 0;
 
-int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const void* xv, const MoeGroups& g,
-                    void* y, int n, int k, cudaStream_t stream) {
-    void* flags = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&flags, g_moe_gemm_fault_flags);
-    if (e != cudaSuccess) return cuda_failure(e);
-    const __half* x = static_cast<const __half*>(xv);
-    const dim3 grid((n + 7) / 8, g.experts);
-    const uint8_t* a = static_cast<const uint8_t*>(w);
-    const uint8_t* b = static_cast<const uint8_t*>(w2);
-    if (w2 != nullptr)
-        q4k_moe_rows_kernel<__half, __half, true, true><<<grid, kMoeRowsThreads, 0, stream>>>(
-            a, b, x, g, static_cast<__half*>(y), n, k, static_cast<unsigned*>(flags));
-    else
-        q4k_moe_rows_kernel<__half, float, false, true><<<grid, kMoeRowsThreads, 0, stream>>>(
-            a, b, x, g, static_cast<float*>(y), n, k, static_cast<unsigned*>(flags));
-    e = cudaGetLastError();
+namespace {
+
+constexpr int kBlockSlots = 192;             // most slots per tile: MMA N
+constexpr int kCtaRows = 128;                // W rows per CTA (TMEM lanes)
+constexpr int kWStages = 4;                  // superblock columns in flight
+constexpr int kWStageBytes = kCtaRows * kBlockBytes;
+constexpr int kGroup = 64;                   // weights per step: one quant group of a superblock
+constexpr int kBStages = 9;
+constexpr int kBStageBytes = kBlockSlots / 2 * kGroup * 2;
+constexpr int kBBoxRows = 32;                // rows per TMA box of x in slot order
+constexpr int kABufs = 4;                    // decoded groups: TMEM buffers of 32 columns
+constexpr int kTmemA = 2 * kBlockSlots;      // D buffers first
+constexpr int kMoeTmemCols = 512;
+constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
+static_assert(kTmemA + kABufs * kGroup / 2 == kMoeTmemCols, "TMEM");
+
+// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-11 decode (two
+// sets), 12-19 epilogue (two per lane quarter). Registers move from the first
+// warpgroup and the decode warps to the epilogue's accumulators:
+// 640 x 96 = 128 x 40 + 256 x 80 + 256 x 136 + 768 spare.
+constexpr int kMoeThreads = 640;
+constexpr int kRegsCopy = 40, kRegsDecode = 80, kRegsEpi = 136;
+static_assert(128 * kRegsCopy + 256 * kRegsDecode + 256 * kRegsEpi <= kMoeThreads * 96, "register split");
+
+struct MoeShared {
+    uint64_t w_full[kWStages], w_empty[kWStages];
+    uint64_t b_full[kBStages], b_empty[kBStages];   // b_full: the first CTA's, for both halves
+    uint64_t a_full[kABufs], a_empty[kABufs];       // a_full: the first CTA's
+    uint64_t d_full[2], d_empty[2];                 // d_empty: the first CTA's
+    uint64_t mma_done;
+    uint32_t tmem;
+    int abort;
+    int warp_tiles[8];
+    int tile0[Q4K_MOE_MAX_EXPERTS + 1];             // first tile of each expert
+    int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];   // its slots
+};
+
+constexpr int kMoeSmem = 1024 + kBStages * kBStageBytes + kWStages * kWStageBytes;
+
+struct MoeGemmParams {
+    MoeGroups g;
+    void* y;
+    int n, nsb, row_tiles;
+};
+
+__device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, &g_moe_gemm_fault_flags);
+}
+__device__ __forceinline__ bool moe_wait_cluster(uint64_t* bar, uint32_t parity) {
+    return mbar_wait_bounded_cluster(bar, parity, &g_moe_gemm_fault_flags);
+}
+
+// A walk over the pair's tiles.
+struct TileWalk {
+    int tile, e;            // current tile and its expert
+    int slot0, slots, cols; // its slots, and their number rounded up to 16 (N)
+    int row_tile;
+
+    __device__ __forceinline__ void start() {
+        tile = static_cast<int>(blockIdx.x >> 1);
+        e = 0;
+    }
+    // Fills in the current tile; false past the last.
+    __device__ __forceinline__ bool open(const MoeShared& sh, int experts) {
+        if (tile >= sh.tile0[experts]) return false;
+        while (tile >= sh.tile0[e + 1]) ++e;
+        const int cnt = sh.count[e];
+        const int blocks = (cnt + kBlockSlots - 1) / kBlockSlots;
+        const int local = tile - sh.tile0[e];
+        row_tile = local / blocks;
+        const int b = local - row_tile * blocks;
+        const int s0 = static_cast<int>(static_cast<long long>(cnt) * b / blocks);
+        const int s1 = static_cast<int>(static_cast<long long>(cnt) * (b + 1) / blocks);
+        slot0 = sh.first[e] + s0;
+        slots = s1 - s0;
+        cols = (slots + 15) & ~15;
+        return true;
+    }
+    __device__ __forceinline__ void next() { tile += static_cast<int>(gridDim.x >> 1); }
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four weights of consecutive K from the bytes of `b` (each 0x80 | q << 3),
+// as two fp16 pairs. FOLDED: c = -(dm + 16 dsc), exact; else c = -dm.
+template <bool FOLDED>
+__device__ __forceinline__ void decode4(uint32_t b, float dsc, float c, uint32_t& p0, uint32_t& p1) {
+    // 0x41 : byte : 0 : 0 is the f32 16 + q
+    float2 f0 = make_float2(__uint_as_float(__byte_perm(b, 0x41000000u, 0x7044)),
+                            __uint_as_float(__byte_perm(b, 0x41000000u, 0x7144)));
+    float2 f1 = make_float2(__uint_as_float(__byte_perm(b, 0x41000000u, 0x7244)),
+                            __uint_as_float(__byte_perm(b, 0x41000000u, 0x7344)));
+    if (!FOLDED) {
+        const float2 one = make_float2(1.f, 1.f), off = make_float2(-16.f, -16.f);
+        f0 = ffma2(f0, one, off);
+        f1 = ffma2(f1, one, off);
+    }
+    const float2 s = make_float2(dsc, dsc), k = make_float2(c, c);
+    f0 = ffma2(f0, s, k);
+    f1 = ffma2(f1, s, k);
+    p0 = pack_half2(f0.x, f0.y);
+    p1 = pack_half2(f1.x, f1.y);
+}
+
+// The 64 weights of one quant group (two sub-blocks: low nibbles, high nibbles)
+// as 32 fp16 pairs in K order.
+template <bool FOLDED>
+__device__ __forceinline__ void decode_group(const uint4 q0, const uint4 q1, float dsc0, float dm0, float dsc1,
+                                             float dm1, uint32_t (&out)[32]) {
+    const float c0 = FOLDED ? -fmaf(16.f, dsc0, dm0) : -dm0;
+    const float c1 = FOLDED ? -fmaf(16.f, dsc1, dm1) : -dm1;
+    const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        decode4<FOLDED>(((w[i] << 3) & 0x78787878u) | 0x80808080u, dsc0, c0, out[2 * i], out[2 * i + 1]);
+        decode4<FOLDED>(((w[i] >> 1) & 0x78787878u) | 0x80808080u, dsc1, c1, out[16 + 2 * i], out[16 + 2 * i + 1]);
+    }
+}
+
+// Whether 16 d sc + dmin m is exact in f32 for every 6-bit sc, m: with e, em the
+// exponent fields of d and dmin (subnormals share field 1's unit), the sum is a
+// multiple of 2^(min(e + 4, em)) units of 2^-25 and below 2^(max(e + 11, em + 7)
+// + 1) of the same scale, so 24 bits hold it for -2 <= em - e <= 10. Inf and
+// NaN (field 31) are left to the unfolded form.
+__device__ __forceinline__ bool fold_is_exact(uint32_t dd) {
+    const int e = static_cast<int>((dd >> 10) & 31u), em = static_cast<int>((dd >> 26) & 31u);
+    const int diff = max(em, 1) - max(e, 1);
+    return e < 31 && em < 31 && diff >= -2 && diff <= 10;
+}
+
+template <bool SWIGLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMoeThreads, 1)
+q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
+                    const __grid_constant__ CUtensorMap map_x, const MoeGemmParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* sb = smem;                                  // [stages][96][64] fp16, swizzled
+    uint8_t* sw = smem + kBStages * kBStageBytes;        // [stages][128][144]
+    __shared__ MoeShared sh;
+    volatile int* abort_flag = &sh.abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int experts = p.g.experts, nsb = p.nsb;
+
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int i = 0; i < kWStages; ++i) {
+            mbar_init(&sh.w_full[i], 1);
+            mbar_init(&sh.w_empty[i], 8);                // decode warps
+        }
+        for (int i = 0; i < kBStages; ++i) {
+            mbar_init(&sh.b_full[i], 1);
+            mbar_init(&sh.b_empty[i], 1);
+        }
+        for (int i = 0; i < kABufs; ++i) {
+            mbar_init(&sh.a_full[i], 8);                 // a set's four warps in both CTAs
+            mbar_init(&sh.a_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.d_full[i], 1);
+            mbar_init(&sh.d_empty[i], 16);               // epilogue warps of both CTAs
+        }
+        mbar_init(&sh.mma_done, 1);
+        fence_mbar_init();
+        tma_prefetch_map(&map_w);
+        if (SWIGLU) tma_prefetch_map(&map_w2);
+        tma_prefetch_map(&map_x);
+    }
+    if (warp == 3) tmem_alloc_pair(&sh.tmem, kMoeTmemCols);
+    pdl_launch_dependents();
+    pdl_wait();
+    // Experts' slots and first tiles (a block-wide scan over up to 256 experts).
+    {
+        int tiles = 0;
+        const int e = threadIdx.x;
+        if (e < experts) {
+            const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
+            const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
+            if (!ok && blockIdx.x == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
+            const int cnt = ok ? b - a : 0;
+            sh.first[e] = a;
+            sh.count[e] = cnt;
+            tiles = (cnt + kBlockSlots - 1) / kBlockSlots * p.row_tiles;
+        }
+        int scan = tiles;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
+            if (lane >= off) scan += v;
+        }
+        if (warp < 8 && lane == 31) sh.warp_tiles[warp] = scan;
+        __syncthreads();
+        if (e < experts) {
+            int before = 0;
+            for (int w = 0; w < warp; ++w) before += sh.warp_tiles[w];
+            sh.tile0[e + 1] = before + scan;
+            if (e == 0) sh.tile0[0] = 0;
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp < 4) {
+        regs_lower<kRegsCopy>();
+        if (warp == 0) {
+            // ------------------------------------------------ weight copies
+            if (lane == 0) {
+                int it = 0;
+                TileWalk t;
+                for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
+                    const int per = SWIGLU ? 64 : kCtaRows;
+                    const int row = t.e * p.n + (t.row_tile * 2 + static_cast<int>(rank)) * per;
+                    for (int b = 0; b < nsb && !*abort_flag; ++b, ++it) {
+                        const int s = it % kWStages;
+                        if (it >= kWStages && !moe_wait(&sh.w_empty[s], static_cast<uint32_t>((it / kWStages - 1) & 1))) {
+                            *abort_flag = 1;
+                            break;
+                        }
+                        uint8_t* dst = sw + s * kWStageBytes;
+                        mbar_arrive_expect_tx(&sh.w_full[s], kWStageBytes);
+                        tma_load_3d(dst, &map_w, 0, b, row, &sh.w_full[s]);
+                        if (SWIGLU) tma_load_3d(dst + kWStageBytes / 2, &map_w2, 0, b, row, &sh.w_full[s]);
+                    }
+                }
+                if (*abort_flag)   // copies in flight land before shared memory goes
+                    for (int i = it > kWStages ? it - kWStages : 0; i < it; ++i)
+                        moe_wait(&sh.w_full[i % kWStages], static_cast<uint32_t>((i / kWStages) & 1));
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------ activation copies
+            int it = 0;
+            TileWalk t;
+            const bool gather = p.g.per_row > 0;
+            for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
+                const int half = t.cols / 2;                       // rows of B in each CTA
+                const int r0 = static_cast<int>(rank) * half;      // the first one's place in the block
+                int rows[4] = {0, 0, 0, 0};
+                if (gather && 4 * lane < half) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = r0 + 4 * lane + j;
+                        // columns past the block's slots repeat its first row; a bad entry takes row 0
+                        const int pair = __ldg(p.g.order + t.slot0 + (i < t.slots ? i : 0));
+                        rows[j] = pair >= 0 && pair < p.g.pairs ? pair / p.g.per_row : 0;
+                    }
+                }
+                const int boxes = (half + kBBoxRows - 1) / kBBoxRows;
+                const uint32_t bytes = static_cast<uint32_t>(gather ? half : boxes * kBBoxRows) * kGroup * 2;
+                for (int i = 0; i < 4 * nsb; ++i, ++it) {
+                    const int s = it % kBStages;
+                    bool ok = true;
+                    if (lane == 0) {
+                        ok = !*abort_flag &&
+                             (it < kBStages || moe_wait(&sh.b_empty[s], static_cast<uint32_t>((it / kBStages - 1) & 1)));
+                        if (ok && rank == 0) mbar_arrive_expect_tx(&sh.b_full[s], 2 * bytes);
+                    }
+                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    const uint32_t bar = map_to_rank(&sh.b_full[s], 0);
+                    uint8_t* dst = sb + s * kBStageBytes;
+                    if (gather) {
+                        if (4 * lane < half)
+                            tma_gather4_pair(dst + lane * 4 * kGroup * 2, &map_x, i * kGroup, rows[0], rows[1], rows[2],
+                                             rows[3], bar);
+                    } else if (lane < boxes) {
+                        tma_load_2d_pair(dst + lane * kBBoxRows * kGroup * 2, &map_x, i * kGroup,
+                                         t.slot0 + r0 + lane * kBBoxRows, bar);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (*abort_flag && rank == 0 && lane == 0)
+                for (int i = it > kBStages ? it - kBStages : 0; i < it; ++i)
+                    moe_wait(&sh.b_full[i % kBStages], static_cast<uint32_t>((i / kBStages) & 1));
+        } else if (warp == 2 && rank == 0 && lane == 0) {
+            // ------------------------------------------------ MMA
+            int it = 0, chunk_no = 0;   // steps, accumulations
+            TileWalk t;
+            const int chunk = SWIGLU ? nsb : kPlainChunk;
+            for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
+                const uint32_t idesc = mma_f16_idesc(256, t.cols);
+                for (int i = 0; i < 4 * nsb; ++i, ++it) {
+                    const int a = it % kABufs, s = it % kBStages;
+                    const int dbuf = chunk_no & 1;
+                    const bool fresh = i % (4 * chunk) == 0;
+                    bool ok = !*abort_flag;
+                    if (fresh && chunk_no >= 2)
+                        ok = ok && moe_wait_cluster(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
+                    ok = ok && moe_wait_cluster(&sh.b_full[s], static_cast<uint32_t>((it / kBStages) & 1)) &&
+                         moe_wait_cluster(&sh.a_full[a], static_cast<uint32_t>((it / kABufs) & 1));
+                    if (!ok) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t b0 = smem_addr(sb + s * kBStageBytes);
+                    const uint32_t acol = tmem + kTmemA + a * (kGroup / 2);
+#pragma unroll
+                    for (int kk = 0; kk < kGroup / 16; ++kk)
+                        mma_f16_tmem_a_pair(tmem + dbuf * kBlockSlots, acol + 8 * kk, sw128_kmajor_desc(b0 + 32 * kk),
+                                            idesc, fresh && kk == 0 ? 0u : 1u);
+                    mma_commit_pair(&sh.b_empty[s]);
+                    mma_commit_pair(&sh.a_empty[a]);
+                    if (i + 1 == 4 * nsb || (i + 1) % (4 * chunk) == 0) {
+                        mma_commit_pair(&sh.d_full[dbuf]);
+                        ++chunk_no;
+                    }
+                }
+            }
+            mma_commit_pair_local(&sh.mma_done);
+            moe_wait(&sh.mma_done, 0u);
+        }
+    } else if (warp < 12) {
+        // ---------------------------------------------------- decode
+        regs_lower<kRegsDecode>();
+        const int set = (warp - 4) >> 2, quarter = warp & 3;
+        const int row = SWIGLU ? (lane < 16 ? 0 : 64) + 16 * quarter + (lane & 15) : 32 * quarter + lane;
+        const uint32_t lane_addr = tmem + kTmemA + (static_cast<uint32_t>(32 * quarter) << 16);
+        int it = 0;    // superblocks
+        bool ok = true;
+        TileWalk t;
+        for (t.start(); ok && t.open(sh, experts); t.next()) {
+            for (int b = 0; b < nsb; ++b, ++it) {
+                const int s = it % kWStages;
+                ok = !*abort_flag && moe_wait(&sh.w_full[s], static_cast<uint32_t>((it / kWStages) & 1));
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    *abort_flag = 1;
+                    break;
+                }
+                const uint8_t* src = sw + s * kWStageBytes + row * kBlockBytes;
+                const uint4 hw = *reinterpret_cast<const uint4*>(src);
+                const Header hd = decode_header(hw);
+                const bool folded = __all_sync(0xFFFFFFFFu, fold_is_exact(hw.x));
+#pragma unroll
+                for (int gi = 0; gi < 2; ++gi) {
+                    const int g = 2 * gi + set;           // this set's groups of the superblock
+                    const int a = 2 * gi + set;           // = (4 it + g) % kABufs
+                    float dsc0, dm0, dsc1, dm1;
+                    const uint32_t scw = gi == 0 ? hd.sc_lo : hd.sc_hi, mw = gi == 0 ? hd.m_lo : hd.m_hi;
+                    const int sh0 = 16 * set;
+                    dsc0 = hd.d * small_u32_to_f32((scw >> sh0) & 0xFFu);
+                    dsc1 = hd.d * small_u32_to_f32((scw >> (sh0 + 8)) & 0xFFu);
+                    dm0 = hd.dmin * small_u32_to_f32((mw >> sh0) & 0xFFu);
+                    dm1 = hd.dmin * small_u32_to_f32((mw >> (sh0 + 8)) & 0xFFu);
+                    const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
+                    const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
+                    uint32_t r[32];
+                    if (folded) decode_group<true>(q0, q1, dsc0, dm0, dsc1, dm1, r);
+                    else decode_group<false>(q0, q1, dsc0, dm0, dsc1, dm1, r);
+                    if (gi == 1) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.w_empty[s]);   // this warp has read its rows
+                    }
+                    ok = it == 0 || moe_wait(&sh.a_empty[a], static_cast<uint32_t>((it - 1) & 1));
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        *abort_flag = 1;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    tmem_store_32cols(lane_addr + a * (kGroup / 2), r);
+                    tmem_wait_st();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.a_full[a], 0));
+                }
+                if (!ok) break;
+            }
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        regs_raise<kRegsEpi>();
+        const int quarter = warp & 3, part = (warp - 12) >> 2;
+        constexpr int kPart = kBlockSlots / 2;             // columns per warp
+        const int c0 = part * kPart;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c0;
+        int chunk_no = 0;
+        bool ok = true;
+        TileWalk t;
+        for (t.start(); ok && t.open(sh, experts); t.next()) {
+            // the pairs of this warp's columns, a column per lane and 32-column piece; -1: not stored
+            int pair[kPart / 32];
+#pragma unroll
+            for (int j = 0; j < kPart / 32; ++j) {
+                const int c = c0 + 32 * j + lane;
+                pair[j] = -1;
+                if (c < t.slots) {
+                    const int v = __ldg(p.g.order + t.slot0 + c);
+                    if (v >= 0 && v < p.g.pairs) pair[j] = v;
+                    else if (t.row_tile == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
+                }
+            }
+            if constexpr (SWIGLU) {
+                const int dbuf = chunk_no & 1;
+                ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / 2) & 1));
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    *abort_flag = 1;
+                    break;
+                }
+                ++chunk_no;
+                tc_fence_after_sync();
+                const int feature = (t.row_tile * 2 + static_cast<int>(rank)) * 64 + 16 * quarter + (lane & 15);
+                const bool live = feature < p.n;
+                __half* y = static_cast<__half*>(p.y) + feature;
+                const bool gate = lane < 16;
+#pragma unroll
+                for (int j = 0; j < kPart / 32; ++j) {
+                    if (c0 + 32 * j >= t.cols) break;
+                    uint32_t r[32];
+                    tmem_load_32cols(lane_addr + dbuf * kBlockSlots + 32 * j, r);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        // lanes with gate rows finish column c, lanes with up rows column c + 1
+                        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, gate ? r[c + 1] : r[c], 16);
+                        const float gv = __uint_as_float(gate ? r[c] : other);
+                        const float uv = __uint_as_float(gate ? other : r[c + 1]);
+                        const int pa = __shfl_sync(0xFFFFFFFFu, pair[j], c), pb = __shfl_sync(0xFFFFFFFFu, pair[j], c + 1);
+                        if (live && (gate ? pa : pb) >= 0)
+                            y[static_cast<size_t>(t.slot0 + c0 + 32 * j + c + (gate ? 0 : 1)) * p.n] =
+                                __float2half_rn(silu_mul(gv, uv));
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
+            } else {
+                float acc[kPart];
+#pragma unroll
+                for (int c = 0; c < kPart; ++c) acc[c] = 0.f;
+                for (int b = 0; b < nsb; b += kPlainChunk) {
+                    const int dbuf = chunk_no & 1;
+                    ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / 2) & 1));
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        *abort_flag = 1;
+                        break;
+                    }
+                    ++chunk_no;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int j = 0; j < kPart / 32; ++j) {
+                        if (c0 + 32 * j < t.cols) {
+                            uint32_t r[32];
+                            tmem_load_32cols(lane_addr + dbuf * kBlockSlots + 32 * j, r);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) acc[32 * j + c] += __uint_as_float(r[c]);
+                        }
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
+                }
+                if (!ok) break;
+                const int row = (t.row_tile * 2 + static_cast<int>(rank)) * kCtaRows + 32 * quarter + lane;
+                float* y = static_cast<float*>(p.y) + row;
+#pragma unroll
+                for (int c = 0; c < kPart; ++c) {
+                    const int pr = __shfl_sync(0xFFFFFFFFu, pair[c / 32], c % 32);
+                    if (pr >= 0 && row < p.n) y[static_cast<size_t>(pr) * p.n] = acc[c];
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();   // no arrival or MMA on either CTA's memory is left
+    if (warp == 3) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, kMoeTmemCols);
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// (byte of a superblock, superblock, row) of all experts' rows, boxes of one
+// superblock by box_rows rows.
+bool make_moe_weight_map(CUtensorMap* map, const void* w, long long rows, int nsb, int box_rows) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kBlockBytes), static_cast<cuuint64_t>(nsb),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kBlockBytes), static_cast<cuuint64_t>(nsb) * kBlockBytes};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kBlockBytes), 1u, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Row-major fp16 [rows][k], boxes of 64 elements by box_rows rows (one for
+// gathers), 128-byte swizzle.
+bool make_moe_x_map(CUtensorMap* map, const void* x, int rows, int k, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k) * 2};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kGroup), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const void* x_f16, const MoeGroups& g, void* y,
+                    int n, int k, cudaStream_t stream) {
+    const bool swiglu = w2 != nullptr;
+    const int nsb = k / kQK;
+    const long long rows = static_cast<long long>(g.experts) * n;
+    CUtensorMap mw, mw2, mx;
+    if (encode_tiled() == nullptr || !make_moe_weight_map(&mw, w, rows, nsb, swiglu ? 64 : kCtaRows) ||
+        !make_moe_weight_map(&mw2, swiglu ? w2 : w, rows, nsb, 64) ||
+        !make_moe_x_map(&mx, x_f16, g.x_rows, k, g.per_row > 0 ? 1 : kBBoxRows))
+        return cuda_failure(cudaErrorInvalidValue);
+    MoeGemmParams p{};
+    p.g = g;
+    p.y = y;
+    p.n = n;
+    p.nsb = nsb;
+    const int tile_rows = swiglu ? kCtaRows : 2 * kCtaRows;
+    p.row_tiles = (n + tile_rows - 1) / tile_rows;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
+    cfg.blockDim = dim3(kMoeThreads);
+    cfg.dynamicSmemBytes = kMoeSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<true>, mw, mw2, mx, p)
+                                 : cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<false>, mw, mw2, mx, p);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 
-int moe_gemm_set_attributes() { return Q4K_OK; }
+int moe_gemm_set_attributes() {
+    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem);
+    return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
+}
 
 int read_moe_gemm_fault_flags(unsigned* flags) {
     unsigned v = 0;
