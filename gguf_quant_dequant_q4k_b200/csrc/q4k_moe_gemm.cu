@@ -49,17 +49,20 @@ constexpr int kBlockSlots = 192;             // most slots per tile: MMA N
 constexpr int kCtaRows = 128;                // W rows per CTA (TMEM lanes)
 constexpr int kWStages = 4;                  // superblock columns in flight
 constexpr int kWStageBytes = kCtaRows * kBlockBytes;
-constexpr int kGroup = 64;                   // weights per step: one quant group of a superblock
-constexpr int kBStages = 9;
-constexpr int kBStageBytes = kBlockSlots / 2 * kGroup * 2;
+constexpr int kGroup = 64;                   // weights of one quant group of a superblock
+constexpr int kStep = 2 * kGroup;            // K per step: two groups, one per decode set
+constexpr int kBStages = 5;
+constexpr int kBHalfBytes = kBlockSlots / 2 * kGroup * 2;   // 64 elements of 96 rows
+constexpr int kBStageBytes = 2 * kBHalfBytes;
 constexpr int kBBoxRows = 32;                // rows per TMA box of x in slot order
-constexpr int kABufs = 4;                    // decoded groups: TMEM buffers of 32 columns
+constexpr int kGatherLag = 3;                // steps whose row copies are in flight
+constexpr int kABufs = 4;                    // decoded groups (two steps): TMEM buffers of 32 columns
 constexpr int kTmemA = 2 * kBlockSlots;      // D buffers first
 constexpr int kMoeTmemCols = 512;
 constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
 static_assert(kTmemA + kABufs * kGroup / 2 == kMoeTmemCols, "TMEM");
 
-// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-11 decode (two
+// Warps: 0 weight copies, 1 and 3 activation copies, 2 MMA; 4-11 decode (two
 // sets), 12-19 epilogue (two per lane quarter). Registers move from the first
 // warpgroup and the decode warps to the epilogue's accumulators:
 // 640 x 96 = 128 x 40 + 256 x 80 + 256 x 136 + 768 spare.
@@ -69,8 +72,9 @@ static_assert(128 * kRegsCopy + 256 * kRegsDecode + 256 * kRegsEpi <= kMoeThread
 
 struct MoeShared {
     uint64_t w_full[kWStages], w_empty[kWStages];
-    uint64_t b_full[kBStages], b_empty[kBStages];   // b_full: the first CTA's, for both halves
-    uint64_t a_full[kABufs], a_empty[kABufs];       // a_full: the first CTA's
+    uint64_t b_full[kBStages];                      // the first CTA's, for both halves of B
+    uint64_t done[kBStages];                        // the step's MMAs are complete: B stage and A buffers free
+    uint64_t a_full[2];                             // the first CTA's; even and odd steps
     uint64_t d_full[2], d_empty[2];                 // d_empty: the first CTA's
     uint64_t mma_done;
     uint32_t tmem;
@@ -78,21 +82,21 @@ struct MoeShared {
     int warp_tiles[8];
     int tile0[Q4K_MOE_MAX_EXPERTS + 1];             // first tile of each expert
     int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];   // its slots
+    int rows[2][kBlockSlots / 2];                   // the gathering warps' rows of x
 };
 
 constexpr int kMoeSmem = 1024 + kBStages * kBStageBytes + kWStages * kWStageBytes;
 
 struct MoeGemmParams {
     MoeGroups g;
+    const void* x;      // gathered rows of x
     void* y;
+    size_t row_bytes;   // of x
     int n, nsb, row_tiles;
 };
 
 __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, &g_moe_gemm_fault_flags);
-}
-__device__ __forceinline__ bool moe_wait_cluster(uint64_t* bar, uint32_t parity) {
-    return mbar_wait_bounded_cluster(bar, parity, &g_moe_gemm_fault_flags);
 }
 
 // A walk over the pair's tiles.
@@ -199,14 +203,11 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             mbar_init(&sh.w_empty[i], 8);                // decode warps
         }
         for (int i = 0; i < kBStages; ++i) {
-            mbar_init(&sh.b_full[i], 1);
-            mbar_init(&sh.b_empty[i], 1);
-        }
-        for (int i = 0; i < kABufs; ++i) {
-            mbar_init(&sh.a_full[i], 8);                 // a set's four warps in both CTAs
-            mbar_init(&sh.a_empty[i], 1);
+            mbar_init(&sh.b_full[i], p.g.per_row > 0 ? 4 : 1);   // gathering warps of both CTAs, or one and bytes
+            mbar_init(&sh.done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.a_full[i], 16);                // the decode warps of both CTAs
             mbar_init(&sh.d_full[i], 1);
             mbar_init(&sh.d_empty[i], 16);               // epilogue warps of both CTAs
         }
@@ -279,91 +280,154 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     for (int i = it > kWStages ? it - kWStages : 0; i < it; ++i)
                         moe_wait(&sh.w_full[i % kWStages], static_cast<uint32_t>((i / kWStages) & 1));
             }
-        } else if (warp == 1) {
-            // ------------------------------------------------ activation copies
-            int it = 0;
+        } else if (warp == 2) {
+            // ------------------------------------------------ MMA
+            // The warp runs converged and one elected lane issues, so that the
+            // operands stay in uniform registers. All 512 TMEM columns are the
+            // pair's: its base address is 0.
+            if (rank == 0) {
+                int s = 0, chunk_no = 0;     // B stage; accumulations so far
+                uint32_t b_par = 0, a_par = 0;
+                bool ok = tmem == 0u;
+                const uint64_t desc0 = sw128_kmajor_desc(smem_addr(sb));
+                TileWalk t;
+                for (t.start(); ok && t.open(sh, experts); t.next()) {
+                    const uint32_t idesc = mma_f16_idesc(256, t.cols);
+                    int left = 0;            // superblocks until the accumulation moves on
+#pragma unroll 1
+                    for (int b = 0; ok && b < nsb; ++b) {
+                        const int dbuf = chunk_no & 1;
+                        const bool fresh = left == 0;
+                        if (fresh) {
+                            left = SWIGLU ? nsb : kPlainChunk;
+                            if (chunk_no >= 2)
+                                ok = moe_wait(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
+                        }
+                        const uint32_t dcol = static_cast<uint32_t>(dbuf * kBlockSlots);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && moe_wait(&sh.b_full[s], b_par) && moe_wait(&sh.a_full[h], a_par);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (elect_one()) {
+                                const uint64_t bd = desc0 + static_cast<uint64_t>(s * (kBStageBytes >> 4));
+#pragma unroll
+                                for (int kk = 0; kk < kStep / 16; ++kk)
+                                    mma_f16_tmem_a_pair(dcol, kTmemA + h * (kStep / 2) + 8 * kk,
+                                                        bd + static_cast<uint64_t>((kk >> 2) * (kBHalfBytes >> 4) + 2 * (kk & 3)),
+                                                        idesc, fresh && h == 0 && kk == 0 ? 0u : 1u);
+                                mma_commit_pair(&sh.done[s]);
+                                if (h == 1 && (left == 1 || b + 1 == nsb)) mma_commit_pair(&sh.d_full[dbuf]);
+                            }
+                            __syncwarp();
+                            if (++s == kBStages) {
+                                s = 0;
+                                b_par ^= 1u;
+                            }
+                        }
+                        a_par ^= 1u;
+                        if (--left == 0 || b + 1 == nsb) ++chunk_no;
+                    }
+                }
+                if (!ok) *abort_flag = 1;
+                if (elect_one()) {
+                    mma_commit_pair_local(&sh.mma_done);
+                    moe_wait(&sh.mma_done, 0u);
+                }
+            }
+        } else if (p.g.per_row > 0) {
+            // ------------------------------------------------ activation rows, gathered
+            // Warp 1 fetches the first 64 elements of each step, warp 3 the
+            // last: eight lanes per row, 16 bytes each, to the swizzled place.
+            const int kh = warp >> 1;
+            int s = 0, it = 0;
+            uint32_t par = 1;
+            bool ok = true;
             TileWalk t;
-            const bool gather = p.g.per_row > 0;
-            for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
+            const uint8_t* xb = static_cast<const uint8_t*>(p.x) + kh * kGroup * 2 + (lane & 7) * 16;
+            const uint32_t dst0 = smem_addr(sb) + kh * kBHalfBytes + (lane >> 3) * 128;
+            const uint32_t bar0 = map_to_rank(&sh.b_full[0], 0);
+            int s_done = 0;      // stage of the oldest step not yet handed on
+            auto hand_on = [&] {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(bar0 + 8 * s_done);
+                if (++s_done == kBStages) s_done = 0;
+            };
+            for (t.start(); ok && !*abort_flag && t.open(sh, experts); t.next()) {
                 const int half = t.cols / 2;                       // rows of B in each CTA
                 const int r0 = static_cast<int>(rank) * half;      // the first one's place in the block
-                int rows[4] = {0, 0, 0, 0};
-                if (gather && 4 * lane < half) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int i = r0 + 4 * lane + j;
-                        // columns past the block's slots repeat its first row; a bad entry takes row 0
-                        const int pair = __ldg(p.g.order + t.slot0 + (i < t.slots ? i : 0));
-                        rows[j] = pair >= 0 && pair < p.g.pairs ? pair / p.g.per_row : 0;
+                __syncwarp();
+                for (int r = lane; r < half; r += 32) {
+                    // columns past the block's slots repeat its first row; a bad entry takes row 0
+                    const int pair = __ldg(p.g.order + t.slot0 + (r0 + r < t.slots ? r0 + r : 0));
+                    sh.rows[kh][r] = pair >= 0 && pair < p.g.pairs ? pair / p.g.per_row : 0;
+                }
+                __syncwarp();
+                for (int i = 0; i < 2 * nsb; ++i, ++it) {
+                    if (it >= kBStages) {
+                        ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[s], par));
+                        if (!ok) break;
+                    }
+                    const uint8_t* src = xb + static_cast<size_t>(i) * kStep * 2;
+                    const uint32_t dst = dst0 + s * kBStageBytes;
+#pragma unroll 4
+                    for (int r = lane >> 3; r < half; r += 4)
+                        cp_async16(dst + (r >> 2) * 512 + (((lane ^ r) & 7) << 4),
+                                   src + static_cast<size_t>(sh.rows[kh][r]) * p.row_bytes);
+                    cp_async_commit();
+                    if (it >= kGatherLag) {
+                        cp_async_wait<kGatherLag>();
+                        hand_on();
+                    }
+                    if (++s == kBStages) {
+                        s = 0;
+                        par ^= 1u;
                     }
                 }
+            }
+            cp_async_wait<0>();
+            for (int i = it > kGatherLag ? it - kGatherLag : 0; i < it; ++i) hand_on();
+            if (!ok) *abort_flag = 1;
+        } else if (warp == 1) {
+            // ------------------------------------------------ activation tiles (x in slot order)
+            int s = 0, it = 0;
+            uint32_t par = 1;
+            bool ok = true;
+            TileWalk t;
+            const uint32_t bar0 = map_to_rank(&sh.b_full[0], 0);
+            for (t.start(); ok && !*abort_flag && t.open(sh, experts); t.next()) {
+                const int half = t.cols / 2;
                 const int boxes = (half + kBBoxRows - 1) / kBBoxRows;
-                const uint32_t bytes = static_cast<uint32_t>(gather ? half : boxes * kBBoxRows) * kGroup * 2;
-                for (int i = 0; i < 4 * nsb; ++i, ++it) {
-                    const int s = it % kBStages;
-                    bool ok = true;
-                    if (lane == 0) {
-                        ok = !*abort_flag &&
-                             (it < kBStages || moe_wait(&sh.b_empty[s], static_cast<uint32_t>((it / kBStages - 1) & 1)));
-                        if (ok && rank == 0) mbar_arrive_expect_tx(&sh.b_full[s], 2 * bytes);
+                const int row = t.slot0 + static_cast<int>(rank) * half;
+                for (int i = 0; i < 2 * nsb; ++i, ++it) {
+                    if (it >= kBStages) {
+                        ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[s], par));
+                        if (!ok) break;
                     }
-                    if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-                        *abort_flag = 1;
-                        break;
-                    }
-                    const uint32_t bar = map_to_rank(&sh.b_full[s], 0);
-                    uint8_t* dst = sb + s * kBStageBytes;
-                    if (gather) {
-                        if (4 * lane < half)
-                            tma_gather4_pair(dst + lane * 4 * kGroup * 2, &map_x, i * kGroup, rows[0], rows[1], rows[2],
-                                             rows[3], bar);
-                    } else if (lane < boxes) {
-                        tma_load_2d_pair(dst + lane * kBBoxRows * kGroup * 2, &map_x, i * kGroup,
-                                         t.slot0 + r0 + lane * kBBoxRows, bar);
+                    if (elect_one()) {
+                        if (rank == 0)   // both CTAs' bytes
+                            mbar_arrive_expect_tx(&sh.b_full[s], 2u * 2u * boxes * kBBoxRows * kGroup * 2);
+                        uint8_t* dst = sb + s * kBStageBytes;
+                        for (int j = 0; j < boxes; ++j) {
+                            tma_load_2d_pair(dst + j * kBBoxRows * kGroup * 2, &map_x, i * kStep, row + j * kBBoxRows,
+                                             bar0 + 8 * s);
+                            tma_load_2d_pair(dst + kBHalfBytes + j * kBBoxRows * kGroup * 2, &map_x, i * kStep + kGroup,
+                                             row + j * kBBoxRows, bar0 + 8 * s);
+                        }
                     }
                     __syncwarp();
+                    if (++s == kBStages) {
+                        s = 0;
+                        par ^= 1u;
+                    }
                 }
             }
-            if (*abort_flag && rank == 0 && lane == 0)
+            if (!ok) *abort_flag = 1;
+            if (*abort_flag && rank == 0)   // copies in flight land before shared memory goes
                 for (int i = it > kBStages ? it - kBStages : 0; i < it; ++i)
                     moe_wait(&sh.b_full[i % kBStages], static_cast<uint32_t>((i / kBStages) & 1));
-        } else if (warp == 2 && rank == 0 && lane == 0) {
-            // ------------------------------------------------ MMA
-            int it = 0, chunk_no = 0;   // steps, accumulations
-            TileWalk t;
-            const int chunk = SWIGLU ? nsb : kPlainChunk;
-            for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
-                const uint32_t idesc = mma_f16_idesc(256, t.cols);
-                for (int i = 0; i < 4 * nsb; ++i, ++it) {
-                    const int a = it % kABufs, s = it % kBStages;
-                    const int dbuf = chunk_no & 1;
-                    const bool fresh = i % (4 * chunk) == 0;
-                    bool ok = !*abort_flag;
-                    if (fresh && chunk_no >= 2)
-                        ok = ok && moe_wait_cluster(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
-                    ok = ok && moe_wait_cluster(&sh.b_full[s], static_cast<uint32_t>((it / kBStages) & 1)) &&
-                         moe_wait_cluster(&sh.a_full[a], static_cast<uint32_t>((it / kABufs) & 1));
-                    if (!ok) {
-                        *abort_flag = 1;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t b0 = smem_addr(sb + s * kBStageBytes);
-                    const uint32_t acol = tmem + kTmemA + a * (kGroup / 2);
-#pragma unroll
-                    for (int kk = 0; kk < kGroup / 16; ++kk)
-                        mma_f16_tmem_a_pair(tmem + dbuf * kBlockSlots, acol + 8 * kk, sw128_kmajor_desc(b0 + 32 * kk),
-                                            idesc, fresh && kk == 0 ? 0u : 1u);
-                    mma_commit_pair(&sh.b_empty[s]);
-                    mma_commit_pair(&sh.a_empty[a]);
-                    if (i + 1 == 4 * nsb || (i + 1) % (4 * chunk) == 0) {
-                        mma_commit_pair(&sh.d_full[dbuf]);
-                        ++chunk_no;
-                    }
-                }
-            }
-            mma_commit_pair_local(&sh.mma_done);
-            moe_wait(&sh.mma_done, 0u);
         }
     } else if (warp < 12) {
         // ---------------------------------------------------- decode
@@ -371,58 +435,63 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         const int set = (warp - 4) >> 2, quarter = warp & 3;
         const int row = SWIGLU ? (lane < 16 ? 0 : 64) + 16 * quarter + (lane & 15) : 32 * quarter + lane;
         const uint32_t lane_addr = tmem + kTmemA + (static_cast<uint32_t>(32 * quarter) << 16);
-        int it = 0;    // superblocks
-        bool ok = true;
+        const uint32_t full0 = map_to_rank(&sh.a_full[0], 0);
+        int ws = 0, ds = 0;                  // weight stage; done barrier of two steps before
+        uint32_t w_par = 0, d_par = 0;
+        bool first = true, ok = true;
         TileWalk t;
         for (t.start(); ok && t.open(sh, experts); t.next()) {
-            for (int b = 0; b < nsb; ++b, ++it) {
-                const int s = it % kWStages;
-                ok = !*abort_flag && moe_wait(&sh.w_full[s], static_cast<uint32_t>((it / kWStages) & 1));
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    *abort_flag = 1;
-                    break;
-                }
-                const uint8_t* src = sw + s * kWStageBytes + row * kBlockBytes;
+#pragma unroll 1
+            for (int b = 0; b < nsb; ++b) {
+                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], w_par));
+                if (!ok) break;
+                const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
                 const uint4 hw = *reinterpret_cast<const uint4*>(src);
                 const Header hd = decode_header(hw);
                 const bool folded = __all_sync(0xFFFFFFFFu, fold_is_exact(hw.x));
-#pragma unroll
-                for (int gi = 0; gi < 2; ++gi) {
-                    const int g = 2 * gi + set;           // this set's groups of the superblock
-                    const int a = 2 * gi + set;           // = (4 it + g) % kABufs
-                    float dsc0, dm0, dsc1, dm1;
-                    const uint32_t scw = gi == 0 ? hd.sc_lo : hd.sc_hi, mw = gi == 0 ? hd.m_lo : hd.m_hi;
-                    const int sh0 = 16 * set;
-                    dsc0 = hd.d * small_u32_to_f32((scw >> sh0) & 0xFFu);
-                    dsc1 = hd.d * small_u32_to_f32((scw >> (sh0 + 8)) & 0xFFu);
-                    dm0 = hd.dmin * small_u32_to_f32((mw >> sh0) & 0xFFu);
-                    dm1 = hd.dmin * small_u32_to_f32((mw >> (sh0 + 8)) & 0xFFu);
-                    const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
-                    const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
+                // this set's sub-blocks: scale and min bytes at 16 set, 16 set + 8 of each word
+                const uint32_t sc[2] = {hd.sc_lo >> (16 * set), hd.sc_hi >> (16 * set)};
+                const uint32_t mn[2] = {hd.m_lo >> (16 * set), hd.m_hi >> (16 * set)};
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t scw = h == 0 ? sc[0] : sc[1], mw = h == 0 ? mn[0] : mn[1];
+                    const float dsc0 = hd.d * small_u32_to_f32(scw & 0xFFu);
+                    const float dsc1 = hd.d * small_u32_to_f32((scw >> 8) & 0xFFu);
+                    const float dm0 = hd.dmin * small_u32_to_f32(mw & 0xFFu);
+                    const float dm1 = hd.dmin * small_u32_to_f32((mw >> 8) & 0xFFu);
+                    const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set);
+                    const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set + 16);
                     uint32_t r[32];
                     if (folded) decode_group<true>(q0, q1, dsc0, dm0, dsc1, dm1, r);
                     else decode_group<false>(q0, q1, dsc0, dm0, dsc1, dm1, r);
-                    if (gi == 1) {
+                    if (h == 1) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.w_empty[s]);   // this warp has read its rows
+                        if (lane == 0) mbar_arrive(&sh.w_empty[ws]);   // this warp has read its rows
                     }
-                    ok = it == 0 || moe_wait(&sh.a_empty[a], static_cast<uint32_t>((it - 1) & 1));
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        *abort_flag = 1;
-                        break;
+                    if (!first) {        // the step two before has been multiplied: its buffer is free
+                        ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[ds], d_par));
+                        if (!ok) break;
+                        if (++ds == kBStages) {
+                            ds = 0;
+                            d_par ^= 1u;
+                        }
+                        tc_fence_after_sync();
                     }
-                    tc_fence_after_sync();
-                    tmem_store_32cols(lane_addr + a * (kGroup / 2), r);
+                    tmem_store_32cols(lane_addr + h * (kStep / 2) + set * (kGroup / 2), r);
                     tmem_wait_st();
                     tc_fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.a_full[a], 0));
+                    if (lane == 0) mbar_arrive_cluster(full0 + 8 * h);
                 }
                 if (!ok) break;
+                first = false;
+                if (++ws == kWStages) {
+                    ws = 0;
+                    w_par ^= 1u;
+                }
             }
         }
+        if (!ok) *abort_flag = 1;
     } else {
         // ---------------------------------------------------- epilogue
         regs_raise<kRegsEpi>();
@@ -558,8 +627,8 @@ bool make_moe_weight_map(CUtensorMap* map, const void* w, long long rows, int ns
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Row-major fp16 [rows][k], boxes of 64 elements by box_rows rows (one for
-// gathers), 128-byte swizzle.
+// Row-major fp16 [rows][k], boxes of 64 elements by box_rows rows, 128-byte
+// swizzle.
 bool make_moe_x_map(CUtensorMap* map, const void* x, int rows, int k, int box_rows) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k) * 2};
@@ -580,10 +649,12 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
     CUtensorMap mw, mw2, mx;
     if (encode_tiled() == nullptr || !make_moe_weight_map(&mw, w, rows, nsb, swiglu ? 64 : kCtaRows) ||
         !make_moe_weight_map(&mw2, swiglu ? w2 : w, rows, nsb, 64) ||
-        !make_moe_x_map(&mx, x_f16, g.x_rows, k, g.per_row > 0 ? 1 : kBBoxRows))
+        !make_moe_x_map(&mx, x_f16, g.x_rows, k, kBBoxRows))
         return cuda_failure(cudaErrorInvalidValue);
     MoeGemmParams p{};
     p.g = g;
+    p.x = x_f16;
+    p.row_bytes = static_cast<size_t>(k) * 2;
     p.y = y;
     p.n = n;
     p.nsb = nsb;

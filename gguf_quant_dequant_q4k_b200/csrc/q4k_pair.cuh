@@ -1,7 +1,8 @@
 // q4k_pair.cuh -- sm_100a primitives of a CTA pair (a cluster of two CTAs whose
 // tensor cores work on one tile): remote mbarrier arrivals, tensor-core
-// instructions of cta_group::2, TMA loads that signal the pair's first CTA, row
-// gathers, and register reallocation between warp roles. No TMA multicast.
+// instructions of cta_group::2, TMA loads that signal the pair's first CTA,
+// 16-byte async copies, and register reallocation between warp roles. No TMA
+// multicast.
 #pragma once
 
 #include <cstdint>
@@ -30,27 +31,9 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
     return r;
 }
 
-// One arrival on a barrier of any CTA of the cluster (address by map_to_rank),
-// releasing this thread's writes at cluster scope.
+// One arrival on a barrier of any CTA of the cluster (address by map_to_rank).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// mbar_wait_bounded on a barrier that threads of the other CTA arrive at.
-__device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_t parity, unsigned* fault_flags) {
-    for (unsigned i = 0; i < kSpinLimit; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitHintNs)
-            : "memory");
-        if (ok) return true;
-    }
-    atomicOr(fault_flags, kFaultCopyTimeout);
-    return false;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // TMEM of a pair: one warp of each CTA allocates (frees) together.
@@ -104,15 +87,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-// Four rows y0..y3 of a map whose box is one row high, x a multiple of 16
-// bytes, to consecutive box rows at dst; completes as tma_load_2d_pair.
-__device__ __forceinline__ void tma_gather4_pair(void* dst, const CUtensorMap* map, int x, int y0, int y1, int y2,
-                                                 int y3, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(bar)
-        : "memory");
+// 16 bytes global -> shared, asynchronously (both 16-byte aligned), bypassing L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// At most N of this thread's committed groups are still in flight.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int REGS>
