@@ -12,16 +12,18 @@
 //   tiles of all experts, the blocks of a row tile one after another.
 // * A (weights). A producer streams 128 rows x 144 bytes per superblock into a
 //   shared-memory ring (TMA). Two sets of four decode warps (a warp per TMEM
-//   lane quarter, a lane per row) take alternate 64-weight groups: a nibble
-//   becomes the f32 16 + q by one byte permute, the weight one packed fma with
-//   (d*sc, -(dmin*m + 16*d*sc)), rounded once, then cvt to fp16 pairs, stored
-//   to TMEM. The folded constant is exact unless d and dmin are further apart
-//   than 2^10 (or 2^-2); such superblocks take q first (one more fma). The
-//   decoded group feeds all N slots, so decoding (about 750 of the SM's issue
-//   cycles per superblock) hides behind the MMAs for N >= 96 (8 N cycles).
-// * B (activations). 64 elements of N / 2 rows per CTA and step, fetched by row
-//   (TMA gather of four rows) or, for x in slot order, as tiles, in the
-//   128-byte-swizzled layout; the pair's tensor cores share the two halves.
+//   lane quarter, a lane per row) take alternate 64-weight groups: the quants
+//   become f32 through binary16 subnormals, the weight is one packed fma,
+//   rounded once, then cvt to fp16 pairs, stored to TMEM. The decoded group
+//   feeds all N slots, so the decoding hides behind the MMAs (8 N cycles per
+//   superblock) where N is large enough.
+// * B (activations). 128 elements of N / 2 rows per CTA and step, by TMA in the
+//   128-byte-swizzled layout; the pair's tensor cores share the two halves. x
+//   in slot order is read in place; otherwise a copy in slot order is made
+//   first (a launch of its own into a stream-ordered workspace). Measured on
+//   2048 tokens, top 2, 14336x4096: fetching each row inside the kernel with
+//   16-byte async copies took 54 cycles per 512 bytes (1.23 ms in all), with
+//   four-row TMA gathers about 90 cycles (2.8 ms).
 // * D. Two TMEM accumulators of 192 columns take turns: the epilogue empties
 //   one while the MMAs fill the other. The tensor core adds to D by truncation
 //   (measured 1.7e-5 relative over K = 14336); every kPlainChunk superblocks
@@ -54,20 +56,19 @@ constexpr int kStep = 2 * kGroup;            // K per step: two groups, one per 
 constexpr int kBStages = 5;
 constexpr int kBHalfBytes = kBlockSlots / 2 * kGroup * 2;   // 64 elements of 96 rows
 constexpr int kBStageBytes = 2 * kBHalfBytes;
-constexpr int kBBoxRows = 32;                // rows per TMA box of x in slot order
-constexpr int kGatherLag = 3;                // steps whose row copies are in flight
+constexpr int kBBoxRows = 32;                // rows per TMA box of x
 constexpr int kABufs = 4;                    // decoded groups (two steps): TMEM buffers of 32 columns
 constexpr int kTmemA = 2 * kBlockSlots;      // D buffers first
 constexpr int kMoeTmemCols = 512;
 constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
 static_assert(kTmemA + kABufs * kGroup / 2 == kMoeTmemCols, "TMEM");
 
-// Warps: 0 weight copies, 1 and 3 activation copies, 2 MMA; 4-11 decode (two
+// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-11 decode (two
 // sets), 12-19 epilogue (two per lane quarter). Registers move from the first
 // warpgroup and the decode warps to the epilogue's accumulators:
-// 640 x 96 = 128 x 40 + 256 x 80 + 256 x 136 + 768 spare.
+// 640 x 96 = 128 x 48 + 256 x 80 + 256 x 136.
 constexpr int kMoeThreads = 640;
-constexpr int kRegsCopy = 40, kRegsDecode = 80, kRegsEpi = 136;
+constexpr int kRegsCopy = 48, kRegsDecode = 80, kRegsEpi = 136;
 static_assert(128 * kRegsCopy + 256 * kRegsDecode + 256 * kRegsEpi <= kMoeThreads * 96, "register split");
 
 struct MoeShared {
@@ -82,16 +83,13 @@ struct MoeShared {
     int warp_tiles[8];
     int tile0[Q4K_MOE_MAX_EXPERTS + 1];             // first tile of each expert
     int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];   // its slots
-    int rows[2][kBlockSlots / 2];                   // the gathering warps' rows of x
 };
 
 constexpr int kMoeSmem = 1024 + kBStages * kBStageBytes + kWStages * kWStageBytes;
 
 struct MoeGemmParams {
     MoeGroups g;
-    const void* x;      // gathered rows of x
     void* y;
-    size_t row_bytes;   // of x
     int n, nsb, row_tiles;
 };
 
@@ -128,56 +126,37 @@ struct TileWalk {
     __device__ __forceinline__ void next() { tile += static_cast<int>(gridDim.x >> 1); }
 };
 
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
+__device__ __forceinline__ uint32_t pack_half2(float2 v) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four weights of consecutive K from the bytes of `b` (each 0x80 | q << 3),
-// as two fp16 pairs. FOLDED: c = -(dm + 16 dsc), exact; else c = -dm.
-template <bool FOLDED>
-__device__ __forceinline__ void decode4(uint32_t b, float dsc, float c, uint32_t& p0, uint32_t& p1) {
-    // 0x41 : byte : 0 : 0 is the f32 16 + q
-    float2 f0 = make_float2(__uint_as_float(__byte_perm(b, 0x41000000u, 0x7044)),
-                            __uint_as_float(__byte_perm(b, 0x41000000u, 0x7144)));
-    float2 f1 = make_float2(__uint_as_float(__byte_perm(b, 0x41000000u, 0x7244)),
-                            __uint_as_float(__byte_perm(b, 0x41000000u, 0x7344)));
-    if (!FOLDED) {
-        const float2 one = make_float2(1.f, 1.f), off = make_float2(-16.f, -16.f);
-        f0 = ffma2(f0, one, off);
-        f1 = ffma2(f1, one, off);
-    }
-    const float2 s = make_float2(dsc, dsc), k = make_float2(c, c);
-    f0 = ffma2(f0, s, k);
-    f1 = ffma2(f1, s, k);
-    p0 = pack_half2(f0.x, f0.y);
-    p1 = pack_half2(f1.x, f1.y);
+__device__ __forceinline__ float2 widen_half2(uint32_t bits) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&bits));
 }
 
 // The 64 weights of one quant group (two sub-blocks: low nibbles, high nibbles)
-// as 32 fp16 pairs in K order.
-template <bool FOLDED>
+// as 32 fp16 pairs in K order. A masked quant word is a pair of subnormal
+// binary16 values, q * 2^-24 (low nibbles) or q * 2^-20 (high nibbles), which
+// widen to f32 exactly; with 2^24 dsc0 and 2^20 dsc1 (exact) one fma gives the
+// weight dsc*q - dm rounded once, and cvt its binary16.
 __device__ __forceinline__ void decode_group(const uint4 q0, const uint4 q1, float dsc0, float dm0, float dsc1,
                                              float dm1, uint32_t (&out)[32]) {
-    const float c0 = FOLDED ? -fmaf(16.f, dsc0, dm0) : -dm0;
-    const float c1 = FOLDED ? -fmaf(16.f, dsc1, dm1) : -dm1;
+    const float2 s0 = make_float2(dsc0 * 16777216.f, dsc0 * 16777216.f), c0 = make_float2(-dm0, -dm0);
+    const float2 s1 = make_float2(dsc1 * 1048576.f, dsc1 * 1048576.f), c1 = make_float2(-dm1, -dm1);
     const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        decode4<FOLDED>(((w[i] << 3) & 0x78787878u) | 0x80808080u, dsc0, c0, out[2 * i], out[2 * i + 1]);
-        decode4<FOLDED>(((w[i] >> 1) & 0x78787878u) | 0x80808080u, dsc1, c1, out[16 + 2 * i], out[16 + 2 * i + 1]);
+        const uint32_t u = w[i] >> 8;
+        const float2 a = widen_half2(w[i] & 0x000F000Fu), b = widen_half2(u & 0x000F000Fu);   // bytes 0 2, 1 3
+        const float2 c = widen_half2(w[i] & 0x00F000F0u), d = widen_half2(u & 0x00F000F0u);
+        const float2 l0 = ffma2(make_float2(a.x, b.x), s0, c0), l1 = ffma2(make_float2(a.y, b.y), s0, c0);
+        const float2 h0 = ffma2(make_float2(c.x, d.x), s1, c1), h1 = ffma2(make_float2(c.y, d.y), s1, c1);
+        out[2 * i] = pack_half2(l0);
+        out[2 * i + 1] = pack_half2(l1);
+        out[16 + 2 * i] = pack_half2(h0);
+        out[16 + 2 * i + 1] = pack_half2(h1);
     }
-}
-
-// Whether 16 d sc + dmin m is exact in f32 for every 6-bit sc, m: with e, em the
-// exponent fields of d and dmin (subnormals share field 1's unit), the sum is a
-// multiple of 2^(min(e + 4, em)) units of 2^-25 and below 2^(max(e + 11, em + 7)
-// + 1) of the same scale, so 24 bits hold it for -2 <= em - e <= 10. Inf and
-// NaN (field 31) are left to the unfolded form.
-__device__ __forceinline__ bool fold_is_exact(uint32_t dd) {
-    const int e = static_cast<int>((dd >> 10) & 31u), em = static_cast<int>((dd >> 26) & 31u);
-    const int diff = max(em, 1) - max(e, 1);
-    return e < 31 && em < 31 && diff >= -2 && diff <= 10;
 }
 
 template <bool SWIGLU>
@@ -203,7 +182,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             mbar_init(&sh.w_empty[i], 8);                // decode warps
         }
         for (int i = 0; i < kBStages; ++i) {
-            mbar_init(&sh.b_full[i], p.g.per_row > 0 ? 4 : 1);   // gathering warps of both CTAs, or one and bytes
+            mbar_init(&sh.b_full[i], 1);
             mbar_init(&sh.done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -336,62 +315,8 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     moe_wait(&sh.mma_done, 0u);
                 }
             }
-        } else if (p.g.per_row > 0) {
-            // ------------------------------------------------ activation rows, gathered
-            // Warp 1 fetches the first 64 elements of each step, warp 3 the
-            // last: eight lanes per row, 16 bytes each, to the swizzled place.
-            const int kh = warp >> 1;
-            int s = 0, it = 0;
-            uint32_t par = 1;
-            bool ok = true;
-            TileWalk t;
-            const uint8_t* xb = static_cast<const uint8_t*>(p.x) + kh * kGroup * 2 + (lane & 7) * 16;
-            const uint32_t dst0 = smem_addr(sb) + kh * kBHalfBytes + (lane >> 3) * 128;
-            const uint32_t bar0 = map_to_rank(&sh.b_full[0], 0);
-            int s_done = 0;      // stage of the oldest step not yet handed on
-            auto hand_on = [&] {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(bar0 + 8 * s_done);
-                if (++s_done == kBStages) s_done = 0;
-            };
-            for (t.start(); ok && !*abort_flag && t.open(sh, experts); t.next()) {
-                const int half = t.cols / 2;                       // rows of B in each CTA
-                const int r0 = static_cast<int>(rank) * half;      // the first one's place in the block
-                __syncwarp();
-                for (int r = lane; r < half; r += 32) {
-                    // columns past the block's slots repeat its first row; a bad entry takes row 0
-                    const int pair = __ldg(p.g.order + t.slot0 + (r0 + r < t.slots ? r0 + r : 0));
-                    sh.rows[kh][r] = pair >= 0 && pair < p.g.pairs ? pair / p.g.per_row : 0;
-                }
-                __syncwarp();
-                for (int i = 0; i < 2 * nsb; ++i, ++it) {
-                    if (it >= kBStages) {
-                        ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[s], par));
-                        if (!ok) break;
-                    }
-                    const uint8_t* src = xb + static_cast<size_t>(i) * kStep * 2;
-                    const uint32_t dst = dst0 + s * kBStageBytes;
-#pragma unroll 4
-                    for (int r = lane >> 3; r < half; r += 4)
-                        cp_async16(dst + (r >> 2) * 512 + (((lane ^ r) & 7) << 4),
-                                   src + static_cast<size_t>(sh.rows[kh][r]) * p.row_bytes);
-                    cp_async_commit();
-                    if (it >= kGatherLag) {
-                        cp_async_wait<kGatherLag>();
-                        hand_on();
-                    }
-                    if (++s == kBStages) {
-                        s = 0;
-                        par ^= 1u;
-                    }
-                }
-            }
-            cp_async_wait<0>();
-            for (int i = it > kGatherLag ? it - kGatherLag : 0; i < it; ++i) hand_on();
-            if (!ok) *abort_flag = 1;
         } else if (warp == 1) {
-            // ------------------------------------------------ activation tiles (x in slot order)
+            // ------------------------------------------------ activation copies
             int s = 0, it = 0;
             uint32_t par = 1;
             bool ok = true;
@@ -446,9 +371,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], w_par));
                 if (!ok) break;
                 const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
-                const uint4 hw = *reinterpret_cast<const uint4*>(src);
-                const Header hd = decode_header(hw);
-                const bool folded = __all_sync(0xFFFFFFFFu, fold_is_exact(hw.x));
+                const Header hd = decode_header(*reinterpret_cast<const uint4*>(src));
                 // this set's sub-blocks: scale and min bytes at 16 set, 16 set + 8 of each word
                 const uint32_t sc[2] = {hd.sc_lo >> (16 * set), hd.sc_hi >> (16 * set)};
                 const uint32_t mn[2] = {hd.m_lo >> (16 * set), hd.m_hi >> (16 * set)};
@@ -462,8 +385,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set);
                     const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set + 16);
                     uint32_t r[32];
-                    if (folded) decode_group<true>(q0, q1, dsc0, dm0, dsc1, dm1, r);
-                    else decode_group<false>(q0, q1, dsc0, dm0, dsc1, dm1, r);
+                    decode_group(q0, q1, dsc0, dm0, dsc1, dm1, r);
                     if (h == 1) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.w_empty[ws]);   // this warp has read its rows
@@ -564,12 +486,13 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     ++chunk_no;
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int j = 0; j < kPart / 32; ++j) {
-                        if (c0 + 32 * j < t.cols) {
-                            uint32_t r[32];
-                            tmem_load_32cols(lane_addr + dbuf * kBlockSlots + 32 * j, r);
+                    for (int j = 0; j < kPart / 16; ++j) {
+                        if (c0 + 16 * j < t.cols) {
+                            uint32_t r[16];
+                            tmem_load_16cols(lane_addr + dbuf * kBlockSlots + 16 * j, r);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) acc[32 * j + c] += __uint_as_float(r[c]);
+                            for (int c = 0; c < 16; ++c) acc[16 * j + c] += __uint_as_float(r[c]);
                         }
                     }
                     tc_fence_before_sync();
@@ -595,6 +518,26 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     if (warp == 3) {
         tc_fence_after_sync();
         tmem_dealloc_pair(tmem, kMoeTmemCols);
+    }
+}
+
+// out[s] = x[order[s] / per_row], s < offsets[experts], 16 bytes per thread and
+// step. A bad entry takes row 0 (the product does not store its slot).
+constexpr int kGatherThreads = 256;
+
+__global__ void __launch_bounds__(kGatherThreads)
+q4k_moe_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, const MoeGroups g, int row16) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int slots = min(g.pairs, __ldg(g.offsets + g.experts));
+    const long long total = static_cast<long long>(slots) * row16;
+    const long long stride = static_cast<long long>(gridDim.x) * kGatherThreads;
+    for (long long i = static_cast<long long>(blockIdx.x) * kGatherThreads + threadIdx.x; i < total; i += stride) {
+        const long long s = i / row16;
+        const int c = static_cast<int>(i - s * row16);
+        const int pair = __ldg(g.order + s);
+        const int row = pair >= 0 && pair < g.pairs ? pair / g.per_row : 0;
+        out[i] = __ldg(x + static_cast<long long>(row) * row16 + c);
     }
 }
 
@@ -646,32 +589,51 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
     const bool swiglu = w2 != nullptr;
     const int nsb = k / kQK;
     const long long rows = static_cast<long long>(g.experts) * n;
-    CUtensorMap mw, mw2, mx;
-    if (encode_tiled() == nullptr || !make_moe_weight_map(&mw, w, rows, nsb, swiglu ? 64 : kCtaRows) ||
-        !make_moe_weight_map(&mw2, swiglu ? w2 : w, rows, nsb, 64) ||
-        !make_moe_x_map(&mx, x_f16, g.x_rows, k, kBBoxRows))
-        return cuda_failure(cudaErrorInvalidValue);
-    MoeGemmParams p{};
-    p.g = g;
-    p.x = x_f16;
-    p.row_bytes = static_cast<size_t>(k) * 2;
-    p.y = y;
-    p.n = n;
-    p.nsb = nsb;
-    const int tile_rows = swiglu ? kCtaRows : 2 * kCtaRows;
-    p.row_tiles = (n + tile_rows - 1) / tile_rows;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
-    cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = kMoeSmem;
-    cfg.stream = stream;
+    if (encode_tiled() == nullptr) return cuda_failure(cudaErrorInvalidValue);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<true>, mw, mw2, mx, p)
-                                 : cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<false>, mw, mw2, mx, p);
+
+    const void* xs = x_f16;      // rows in slot order
+    void* work = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (g.per_row > 0) {
+        e = cudaMallocAsync(&work, static_cast<size_t>(g.pairs) * static_cast<size_t>(k) * 2, stream);
+        if (e != cudaSuccess) return cuda_failure(e);
+        const long long blocks = (static_cast<long long>(g.pairs) * (k / 8) + kGatherThreads - 1) / kGatherThreads;
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks < dev.sm_count * 8 ? blocks : dev.sm_count * 8));
+        cfg.blockDim = dim3(kGatherThreads);
+        e = cudaLaunchKernelEx(&cfg, q4k_moe_gather_kernel, static_cast<const uint4*>(x_f16), static_cast<uint4*>(work), g,
+                               k / 8);
+        xs = work;
+    }
+    CUtensorMap mw, mw2, mx;
+    if (e == cudaSuccess &&
+        (!make_moe_weight_map(&mw, w, rows, nsb, swiglu ? 64 : kCtaRows) ||
+         !make_moe_weight_map(&mw2, swiglu ? w2 : w, rows, nsb, 64) || !make_moe_x_map(&mx, xs, g.pairs, k, kBBoxRows)))
+        e = cudaErrorInvalidValue;
+    if (e == cudaSuccess) {
+        MoeGemmParams p{};
+        p.g = g;
+        p.y = y;
+        p.n = n;
+        p.nsb = nsb;
+        const int tile_rows = swiglu ? kCtaRows : 2 * kCtaRows;
+        p.row_tiles = (n + tile_rows - 1) / tile_rows;
+        cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
+        cfg.blockDim = dim3(kMoeThreads);
+        cfg.dynamicSmemBytes = kMoeSmem;
+        e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<true>, mw, mw2, mx, p)
+                   : cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<false>, mw, mw2, mx, p);
+    }
+    if (work != nullptr) {
+        const cudaError_t f = cudaFreeAsync(work, stream);
+        if (e == cudaSuccess) e = f;
+    }
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 

@@ -1,8 +1,7 @@
 // q4k_pair.cuh -- sm_100a primitives of a CTA pair (a cluster of two CTAs whose
 // tensor cores work on one tile): remote mbarrier arrivals, tensor-core
-// instructions of cta_group::2, TMA loads that signal the pair's first CTA,
-// 16-byte async copies, and register reallocation between warp roles. No TMA
-// multicast.
+// instructions of cta_group::2, TMA loads that signal the pair's first CTA, and
+// register reallocation between warp roles. No TMA multicast.
 #pragma once
 
 #include <cstdint>
@@ -85,17 +84,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
-}
-
-// 16 bytes global -> shared, asynchronously (both 16-byte aligned), bypassing L1.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// At most N of this thread's committed groups are still in flight.
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int REGS>
