@@ -11,9 +11,9 @@
 //   (l < 16) hold gate and up of one feature. 74 persistent pairs walk the
 //   tiles of all experts, the blocks of a row tile one after another.
 // * A (weights). A producer streams 128 rows x 144 bytes per superblock into a
-//   shared-memory ring (TMA). Two sets of four decode warps (a warp per TMEM
-//   lane quarter, a lane per row) take alternate 64-weight groups: the quants
-//   become f32 through binary16 subnormals, the weight is one packed fma,
+//   shared-memory ring (TMA). Three sets of four decode warps (a warp per TMEM
+//   lane quarter, a lane per row) take the 64-weight quant groups in turn: the
+//   quants become f32 through binary16 subnormals, the weight is one packed fma,
 //   rounded once, then cvt to fp16 pairs, stored to TMEM. The decoded group
 //   feeds all N slots, so the decoding hides behind the MMAs (8 N cycles per
 //   superblock) where N is large enough.
@@ -34,6 +34,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_fp16.h>
+#include <mutex>
 
 #include "q4k_internal.h"
 #include "q4k_moe.h"
@@ -63,19 +64,24 @@ constexpr int kMoeTmemCols = 512;
 constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
 static_assert(kTmemA + kABufs * kGroup / 2 == kMoeTmemCols, "TMEM");
 
-// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-11 decode (two
-// sets), 12-19 epilogue (two per lane quarter). Registers move from the first
-// warpgroup and the decode warps to the epilogue's accumulators:
-// 640 x 96 = 128 x 48 + 256 x 80 + 256 x 136.
-constexpr int kMoeThreads = 640;
-constexpr int kRegsCopy = 48, kRegsDecode = 80, kRegsEpi = 136;
-static_assert(128 * kRegsCopy + 256 * kRegsDecode + 256 * kRegsEpi <= kMoeThreads * 96, "register split");
+// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-15 decode (three
+// sets of a warp per lane quarter); 16-23 epilogue (two per lane quarter).
+// Registers move from the others to the epilogue's accumulators:
+// 768 x 80 = 128 x 32 + 384 x 64 + 256 x 128. Three sets, not two: the decode
+// is bound by the latency of its chains (a step's two groups take 626 cycles on
+// 8 warps of an SM, 507 on 12, 499 on 16).
+constexpr int kSets = 3;
+constexpr int kDecodeWarp0 = 4, kEpiWarp0 = kDecodeWarp0 + 4 * kSets;
+constexpr int kMoeThreads = 32 * (kEpiWarp0 + 8);
+constexpr int kRegsLaunch = 80, kRegsCopy = 32, kRegsDecode = 64, kRegsEpi = 128;
+static_assert(kMoeThreads * kRegsLaunch <= 65536 &&
+                  128 * kRegsCopy + 128 * kSets * kRegsDecode + 256 * kRegsEpi <= kMoeThreads * kRegsLaunch,
+              "register split");
 
 struct MoeShared {
     uint64_t w_full[kWStages], w_empty[kWStages];
-    uint64_t b_full[kBStages];                      // the first CTA's, for both halves of B
+    uint64_t full[kBStages];                        // the first CTA's: both CTAs' A and B of the step are there
     uint64_t done[kBStages];                        // the step's MMAs are complete: B stage and A buffers free
-    uint64_t a_full[2];                             // the first CTA's; even and odd steps
     uint64_t d_full[2], d_empty[2];                 // d_empty: the first CTA's
     uint64_t mma_done;
     uint32_t tmem;
@@ -179,14 +185,13 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         sh.abort = 0;
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], 8);                // decode warps
+            mbar_init(&sh.w_empty[i], 4 * kSets);        // decode warps
         }
         for (int i = 0; i < kBStages; ++i) {
-            mbar_init(&sh.b_full[i], 1);
+            mbar_init(&sh.full[i], 17);                  // B's bytes; two groups' decode warps in both CTAs
             mbar_init(&sh.done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.a_full[i], 16);                // the decode warps of both CTAs
             mbar_init(&sh.d_full[i], 1);
             mbar_init(&sh.d_empty[i], 16);               // epilogue warps of both CTAs
         }
@@ -265,48 +270,42 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             // operands stay in uniform registers. All 512 TMEM columns are the
             // pair's: its base address is 0.
             if (rank == 0) {
+                const int chunk = SWIGLU ? nsb : kPlainChunk;   // superblocks per accumulation
                 int s = 0, chunk_no = 0;     // B stage; accumulations so far
-                uint32_t b_par = 0, a_par = 0;
+                uint32_t par = 0;
                 bool ok = tmem == 0u;
                 const uint64_t desc0 = sw128_kmajor_desc(smem_addr(sb));
                 TileWalk t;
                 for (t.start(); ok && t.open(sh, experts); t.next()) {
                     const uint32_t idesc = mma_f16_idesc(256, t.cols);
-                    int left = 0;            // superblocks until the accumulation moves on
-#pragma unroll 1
-                    for (int b = 0; ok && b < nsb; ++b) {
+                    for (int b = 0; ok && b < nsb; b += chunk, ++chunk_no) {
                         const int dbuf = chunk_no & 1;
-                        const bool fresh = left == 0;
-                        if (fresh) {
-                            left = SWIGLU ? nsb : kPlainChunk;
-                            if (chunk_no >= 2)
-                                ok = moe_wait(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
-                        }
+                        if (chunk_no >= 2)
+                            ok = moe_wait(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
                         const uint32_t dcol = static_cast<uint32_t>(dbuf * kBlockSlots);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            ok = ok && moe_wait(&sh.b_full[s], b_par) && moe_wait(&sh.a_full[h], a_par);
-                            ok = __all_sync(0xFFFFFFFFu, ok);
+                        const int steps = 2 * min(chunk, nsb - b);
+#pragma unroll 1
+                        for (int i = 0; i < steps; ++i) {
+                            ok = __all_sync(0xFFFFFFFFu, ok && moe_wait(&sh.full[s], par));
                             if (!ok) break;
                             tc_fence_after_sync();
                             if (elect_one()) {
                                 const uint64_t bd = desc0 + static_cast<uint64_t>(s * (kBStageBytes >> 4));
+                                const uint32_t acol = kTmemA + (i & 1) * (kStep / 2);
 #pragma unroll
                                 for (int kk = 0; kk < kStep / 16; ++kk)
-                                    mma_f16_tmem_a_pair(dcol, kTmemA + h * (kStep / 2) + 8 * kk,
+                                    mma_f16_tmem_a_pair(dcol, acol + 8 * kk,
                                                         bd + static_cast<uint64_t>((kk >> 2) * (kBHalfBytes >> 4) + 2 * (kk & 3)),
-                                                        idesc, fresh && h == 0 && kk == 0 ? 0u : 1u);
+                                                        idesc, i == 0 && kk == 0 ? 0u : 1u);
                                 mma_commit_pair(&sh.done[s]);
-                                if (h == 1 && (left == 1 || b + 1 == nsb)) mma_commit_pair(&sh.d_full[dbuf]);
+                                if (i + 1 == steps) mma_commit_pair(&sh.d_full[dbuf]);
                             }
                             __syncwarp();
                             if (++s == kBStages) {
                                 s = 0;
-                                b_par ^= 1u;
+                                par ^= 1u;
                             }
                         }
-                        a_par ^= 1u;
-                        if (--left == 0 || b + 1 == nsb) ++chunk_no;
                     }
                 }
                 if (!ok) *abort_flag = 1;
@@ -321,7 +320,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             uint32_t par = 1;
             bool ok = true;
             TileWalk t;
-            const uint32_t bar0 = map_to_rank(&sh.b_full[0], 0);
+            const uint32_t bar0 = map_to_rank(&sh.full[0], 0);
             for (t.start(); ok && !*abort_flag && t.open(sh, experts); t.next()) {
                 const int half = t.cols / 2;
                 const int boxes = (half + kBBoxRows - 1) / kBBoxRows;
@@ -333,7 +332,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     }
                     if (elect_one()) {
                         if (rank == 0)   // both CTAs' bytes
-                            mbar_arrive_expect_tx(&sh.b_full[s], 2u * 2u * boxes * kBBoxRows * kGroup * 2);
+                            mbar_arrive_expect_tx(&sh.full[s], 2u * 2u * boxes * kBBoxRows * kGroup * 2);
                         uint8_t* dst = sb + s * kBStageBytes;
                         for (int j = 0; j < boxes; ++j) {
                             tma_load_2d_pair(dst + j * kBBoxRows * kGroup * 2, &map_x, i * kStep, row + j * kBBoxRows,
@@ -350,74 +349,66 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 }
             }
             if (!ok) *abort_flag = 1;
-            if (*abort_flag && rank == 0)   // copies in flight land before shared memory goes
-                for (int i = it > kBStages ? it - kBStages : 0; i < it; ++i)
-                    moe_wait(&sh.b_full[i % kBStages], static_cast<uint32_t>((i / kBStages) & 1));
+            if (*abort_flag) {   // copies in flight land before shared memory goes: their bytes are
+                                 // counted on barriers that may now miss arrivals, so wait them out
+                for (int i = 0; i < 64; ++i) __nanosleep(1000000);
+            }
         }
-    } else if (warp < 12) {
+    } else if (warp < kEpiWarp0) {
         // ---------------------------------------------------- decode
+        // The pair's quant groups in the order of its tiles are numbered
+        // through: group i is decoded by set i % 3 into TMEM buffer i % 4 for
+        // step i / 2.
         regs_lower<kRegsDecode>();
-        const int set = (warp - 4) >> 2, quarter = warp & 3;
+        const int quarter = warp & 3;
         const int row = SWIGLU ? (lane < 16 ? 0 : 64) + 16 * quarter + (lane & 15) : 32 * quarter + lane;
         const uint32_t lane_addr = tmem + kTmemA + (static_cast<uint32_t>(32 * quarter) << 16);
-        const uint32_t full0 = map_to_rank(&sh.a_full[0], 0);
-        int ws = 0, ds = 0;                  // weight stage; done barrier of two steps before
-        uint32_t w_par = 0, d_par = 0;
-        bool first = true, ok = true;
-        TileWalk t;
-        for (t.start(); ok && t.open(sh, experts); t.next()) {
+        const uint32_t full0 = map_to_rank(&sh.full[0], 0);
+        const int pairs = static_cast<int>(gridDim.x >> 1), pair = static_cast<int>(blockIdx.x >> 1);
+        const int tiles = sh.tile0[experts] > pair ? (sh.tile0[experts] - pair - 1) / pairs + 1 : 0;
+        const uint32_t groups = 4u * static_cast<uint32_t>(tiles) * static_cast<uint32_t>(nsb);
+        uint32_t have = ~0u;                 // superblock whose header is in hd
+        Header hd{};
+        bool ok = true;
 #pragma unroll 1
-            for (int b = 0; b < nsb; ++b) {
-                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], w_par));
+        for (uint32_t i = (warp - kDecodeWarp0) >> 2; i < groups; i += kSets) {
+            const uint32_t b = i >> 2, g = i & 3u, ws = b % kWStages;
+            const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
+            if (b != have) {
+                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], (b / kWStages) & 1u));
                 if (!ok) break;
-                const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
-                const Header hd = decode_header(*reinterpret_cast<const uint4*>(src));
-                // this set's sub-blocks: scale and min bytes at 16 set, 16 set + 8 of each word
-                const uint32_t sc[2] = {hd.sc_lo >> (16 * set), hd.sc_hi >> (16 * set)};
-                const uint32_t mn[2] = {hd.m_lo >> (16 * set), hd.m_hi >> (16 * set)};
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t scw = h == 0 ? sc[0] : sc[1], mw = h == 0 ? mn[0] : mn[1];
-                    const float dsc0 = hd.d * small_u32_to_f32(scw & 0xFFu);
-                    const float dsc1 = hd.d * small_u32_to_f32((scw >> 8) & 0xFFu);
-                    const float dm0 = hd.dmin * small_u32_to_f32(mw & 0xFFu);
-                    const float dm1 = hd.dmin * small_u32_to_f32((mw >> 8) & 0xFFu);
-                    const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set);
-                    const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 64 * h + 32 * set + 16);
-                    uint32_t r[32];
-                    decode_group(q0, q1, dsc0, dm0, dsc1, dm1, r);
-                    if (h == 1) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.w_empty[ws]);   // this warp has read its rows
-                    }
-                    if (!first) {        // the step two before has been multiplied: its buffer is free
-                        ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[ds], d_par));
-                        if (!ok) break;
-                        if (++ds == kBStages) {
-                            ds = 0;
-                            d_par ^= 1u;
-                        }
-                        tc_fence_after_sync();
-                    }
-                    tmem_store_32cols(lane_addr + h * (kStep / 2) + set * (kGroup / 2), r);
-                    tmem_wait_st();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(full0 + 8 * h);
-                }
-                if (!ok) break;
-                first = false;
-                if (++ws == kWStages) {
-                    ws = 0;
-                    w_par ^= 1u;
-                }
+                hd = decode_header(*reinterpret_cast<const uint4*>(src));
+                have = b;
             }
+            const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
+            const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
+            // sub-blocks 2g and 2g + 1
+            const uint32_t scw = (g < 2 ? hd.sc_lo : hd.sc_hi) >> (16 * (g & 1));
+            const uint32_t mw = (g < 2 ? hd.m_lo : hd.m_hi) >> (16 * (g & 1));
+            uint32_t r[32];
+            decode_group(q0, q1, hd.d * small_u32_to_f32(scw & 0xFFu), hd.dmin * small_u32_to_f32(mw & 0xFFu),
+                         hd.d * small_u32_to_f32((scw >> 8) & 0xFFu), hd.dmin * small_u32_to_f32((mw >> 8) & 0xFFu), r);
+            if ((i + kSets) >> 2 != b) {     // this warp's last group of the superblock
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.w_empty[ws]);
+            }
+            if (i >= kABufs) {               // the buffer's last step has been multiplied
+                const uint32_t step = (i - kABufs) >> 1;
+                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[step % kBStages], (step / kBStages) & 1u));
+                if (!ok) break;
+                tc_fence_after_sync();
+            }
+            tmem_store_32cols(lane_addr + (i % kABufs) * (kGroup / 2), r);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(full0 + 8 * ((i >> 1) % kBStages));
         }
         if (!ok) *abort_flag = 1;
     } else {
         // ---------------------------------------------------- epilogue
         regs_raise<kRegsEpi>();
-        const int quarter = warp & 3, part = (warp - 12) >> 2;
+        const int quarter = warp & 3, part = (warp - kEpiWarp0) >> 2;
         constexpr int kPart = kBlockSlots / 2;             // columns per warp
         const int c0 = part * kPart;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c0;
@@ -427,6 +418,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         for (t.start(); ok && t.open(sh, experts); t.next()) {
             // the pairs of this warp's columns, a column per lane and 32-column piece; -1: not stored
             int pair[kPart / 32];
+            uint32_t stored[kPart / 32];   // columns with one, as bits
 #pragma unroll
             for (int j = 0; j < kPart / 32; ++j) {
                 const int c = c0 + 32 * j + lane;
@@ -436,6 +428,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (v >= 0 && v < p.g.pairs) pair[j] = v;
                     else if (t.row_tile == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
                 }
+                stored[j] = __ballot_sync(0xFFFFFFFFu, pair[j] >= 0);
             }
             if constexpr (SWIGLU) {
                 const int dbuf = chunk_no & 1;
@@ -448,24 +441,22 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 ++chunk_no;
                 tc_fence_after_sync();
                 const int feature = (t.row_tile * 2 + static_cast<int>(rank)) * 64 + 16 * quarter + (lane & 15);
-                const bool live = feature < p.n;
-                __half* y = static_cast<__half*>(p.y) + feature;
                 const bool gate = lane < 16;
+                // lanes with gate rows finish even columns, lanes with up rows odd ones
+                __half* y = static_cast<__half*>(p.y) + static_cast<size_t>(t.slot0 + c0 + (gate ? 0 : 1)) * p.n + feature;
 #pragma unroll
                 for (int j = 0; j < kPart / 32; ++j) {
                     if (c0 + 32 * j >= t.cols) break;
                     uint32_t r[32];
                     tmem_load_32cols(lane_addr + dbuf * kBlockSlots + 32 * j, r);
+                    const uint32_t mine = feature < p.n ? stored[j] >> (gate ? 0 : 1) : 0u;
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        // lanes with gate rows finish column c, lanes with up rows column c + 1
                         const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, gate ? r[c + 1] : r[c], 16);
                         const float gv = __uint_as_float(gate ? r[c] : other);
                         const float uv = __uint_as_float(gate ? other : r[c + 1]);
-                        const int pa = __shfl_sync(0xFFFFFFFFu, pair[j], c), pb = __shfl_sync(0xFFFFFFFFu, pair[j], c + 1);
-                        if (live && (gate ? pa : pb) >= 0)
-                            y[static_cast<size_t>(t.slot0 + c0 + 32 * j + c + (gate ? 0 : 1)) * p.n] =
-                                __float2half_rn(silu_mul(gv, uv));
+                        if (mine & (1u << c))
+                            y[static_cast<size_t>(32 * j + c) * p.n] = __float2half_rn(silu_mul_fast(gv, uv));
                     }
                 }
                 tc_fence_before_sync();
@@ -486,13 +477,13 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     ++chunk_no;
                     tc_fence_after_sync();
 #pragma unroll
-                    for (int j = 0; j < kPart / 16; ++j) {
-                        if (c0 + 16 * j < t.cols) {
-                            uint32_t r[16];
-                            tmem_load_16cols(lane_addr + dbuf * kBlockSlots + 16 * j, r);
+                    for (int j = 0; j < kPart / 8; ++j) {
+                        if (c0 + 8 * j < t.cols) {
+                            uint32_t r[8];
+                            tmem_load_8cols(lane_addr + dbuf * kBlockSlots + 8 * j, r);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) acc[16 * j + c] += __uint_as_float(r[c]);
+                            for (int c = 0; c < 8; ++c) acc[8 * j + c] += __uint_as_float(r[c]);
                         }
                     }
                     tc_fence_before_sync();
@@ -582,6 +573,32 @@ bool make_moe_x_map(CUtensorMap* map, const void* x, int rows, int k, int box_ro
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The current device's pool for the copies of x: it keeps its memory between
+// calls (the default pool gives it back whenever the device is synchronised,
+// and the next allocation then takes 0.5-1.6 ms).
+cudaError_t workspace_pool(cudaMemPool_t* pool) {
+    constexpr int kDevices = 64;
+    static std::once_flag once[kDevices];
+    static cudaMemPool_t pools[kDevices];
+    static cudaError_t status[kDevices];
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        cudaMemPoolProps props = {};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        status[dev] = cudaMemPoolCreate(&pools[dev], &props);
+        uint64_t keep = UINT64_MAX;
+        if (status[dev] == cudaSuccess)
+            status[dev] = cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &keep);
+    });
+    *pool = pools[dev];
+    return status[dev];
+}
+
 }  // namespace
 
 int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const void* x_f16, const MoeGroups& g, void* y,
@@ -602,7 +619,10 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
     void* work = nullptr;
     cudaError_t e = cudaSuccess;
     if (g.per_row > 0) {
-        e = cudaMallocAsync(&work, static_cast<size_t>(g.pairs) * static_cast<size_t>(k) * 2, stream);
+        cudaMemPool_t pool = nullptr;
+        e = workspace_pool(&pool);
+        if (e == cudaSuccess)
+            e = cudaMallocFromPoolAsync(&work, static_cast<size_t>(g.pairs) * static_cast<size_t>(k) * 2, pool, stream);
         if (e != cudaSuccess) return cuda_failure(e);
         const long long blocks = (static_cast<long long>(g.pairs) * (k / 8) + kGatherThreads - 1) / kGatherThreads;
         cfg.gridDim = dim3(static_cast<unsigned>(blocks < dev.sm_count * 8 ? blocks : dev.sm_count * 8));
