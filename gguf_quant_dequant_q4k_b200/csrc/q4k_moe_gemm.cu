@@ -48,40 +48,59 @@ __device__ unsigned int g_moe_gemm_fault_flags = 0;
 
 namespace {
 
-constexpr int kBlockSlots = 192;             // most slots per tile: MMA N
 constexpr int kCtaRows = 128;                // W rows per CTA (TMEM lanes)
-constexpr int kWStages = 4;                  // superblock columns in flight
 constexpr int kWStageBytes = kCtaRows * kBlockBytes;
 constexpr int kGroup = 64;                   // weights of one quant group of a superblock
-constexpr int kStep = 2 * kGroup;            // K per step: two groups, one per decode set
-constexpr int kBStages = 5;
-constexpr int kBHalfBytes = kBlockSlots / 2 * kGroup * 2;   // 64 elements of 96 rows
-constexpr int kBStageBytes = 2 * kBHalfBytes;
+constexpr int kStep = 2 * kGroup;            // K per step
 constexpr int kBBoxRows = 32;                // rows per TMA box of x
-constexpr int kABufs = 4;                    // decoded groups (two steps): TMEM buffers of 32 columns
-constexpr int kTmemA = 2 * kBlockSlots;      // D buffers first
 constexpr int kMoeTmemCols = 512;
 constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
-static_assert(kTmemA + kABufs * kGroup / 2 == kMoeTmemCols, "TMEM");
+constexpr int kMaxWStages = 6, kMaxBStages = 6;
+constexpr int kDecodeWarp0 = 4;
 
-// Warps: 0 weight copies, 1 activation copies, 2 MMA, 3 TMEM; 4-15 decode (three
-// sets of a warp per lane quarter); 16-23 epilogue (two per lane quarter).
-// Registers move from the others to the epilogue's accumulators:
-// 768 x 80 = 128 x 32 + 384 x 64 + 256 x 128. Three sets, not two: the decode
-// is bound by the latency of its chains (a step's two groups take 626 cycles on
-// 8 warps of an SM, 507 on 12, 499 on 16).
-constexpr int kSets = 3;
-constexpr int kDecodeWarp0 = 4, kEpiWarp0 = kDecodeWarp0 + 4 * kSets;
-constexpr int kMoeThreads = 32 * (kEpiWarp0 + 8);
-constexpr int kRegsLaunch = 80, kRegsCopy = 32, kRegsDecode = 64, kRegsEpi = 128;
-static_assert(kMoeThreads * kRegsLaunch <= 65536 &&
-                  128 * kRegsCopy + 128 * kSets * kRegsDecode + 256 * kRegsEpi <= kMoeThreads * kRegsLaunch,
-              "register split");
+// The two shapes of the kernel. Warps: 0 weight copies, 1 activation copies, 2
+// MMA, 3 TMEM; from 4 the decode sets (a warp per lane quarter each); then eight
+// epilogue warps (two per lane quarter).
+// * Wide (large groups): blocks of 256 slots, so that a step's MMAs (1024
+//   cycles) cover the decoding of its weights (650 on two sets) and the issue of
+//   the MMAs (49 cycles each). One accumulator; the epilogue takes it into
+//   registers at once (128 columns per thread) and the MMAs go on.
+// * Narrow (groups of about a hundred or fewer): blocks of 128 slots, where the
+//   decoding sets the pace: three sets (a step's two groups take 626 cycles on 8
+//   warps, 507 on 12, 499 on 16), two accumulators.
+// Both keep four steps of decoded weights in TMEM: with two, the chain MMAs done
+// -> store -> MMAs issued (about 1500 cycles) set the pace (2048 tokens, 14336 x
+// 4096: 1080 cycles per step of 704).
+// Registers move from the copy and decode warps to the epilogue:
+// 640 x 96 = 128 x 48 + 256 x 64 + 256 x 152; 768 x 80 >= 128 x 48 + 384 x 72 +
+// 256 x 104.
+template <bool WIDE>
+struct MoeShape {
+    static constexpr int slots = WIDE ? 256 : 128;           // most slots per tile: MMA N
+    static constexpr int d_bufs = WIDE ? 1 : 2;
+    static constexpr int a_col0 = slots * d_bufs;            // TMEM: D, then A
+    static constexpr int a_bufs = (kMoeTmemCols - a_col0) / (kGroup / 2);   // decoded groups
+    static constexpr int sets = WIDE ? 2 : 3;
+    static constexpr int epi_warp0 = kDecodeWarp0 + 4 * sets;
+    static constexpr int threads = 32 * (epi_warp0 + 8);
+    static constexpr int regs_launch = WIDE ? 96 : 80, regs_copy = 48, regs_decode = WIDE ? 64 : 72,
+                         regs_epi = WIDE ? 152 : 104;
+    static constexpr int b_stages = WIDE ? 4 : 6, w_stages = WIDE ? 4 : 6;
+    static constexpr int b_half = slots / 2 * kGroup * 2;    // 64 elements of the CTA's rows of B
+    static constexpr int b_stage = 2 * b_half;
+    static constexpr int smem = 1024 + b_stages * b_stage + w_stages * kWStageBytes;
+    static_assert(threads * regs_launch <= 65536 &&
+                      128 * regs_copy + 128 * sets * regs_decode + 256 * regs_epi <= threads * regs_launch,
+                  "register split");
+    static_assert(b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
+    static_assert(smem <= 227 * 1024 - 4096, "shared memory");
+};
+constexpr int kNarrowPairsPerExpert = 96;    // at most this many pairs per expert on average: narrow
 
 struct MoeShared {
-    uint64_t w_full[kWStages], w_empty[kWStages];
-    uint64_t full[kBStages];                        // the first CTA's: both CTAs' A and B of the step are there
-    uint64_t done[kBStages];                        // the step's MMAs are complete: B stage and A buffers free
+    uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
+    uint64_t full[kMaxBStages];                     // the first CTA's: both CTAs' A and B of the step are there
+    uint64_t done[kMaxBStages];                     // the step's MMAs are complete: B stage and A buffers free
     uint64_t d_full[2], d_empty[2];                 // d_empty: the first CTA's
     uint64_t mma_done;
     uint32_t tmem;
@@ -90,8 +109,6 @@ struct MoeShared {
     int tile0[Q4K_MOE_MAX_EXPERTS + 1];             // first tile of each expert
     int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];   // its slots
 };
-
-constexpr int kMoeSmem = 1024 + kBStages * kBStageBytes + kWStages * kWStageBytes;
 
 struct MoeGemmParams {
     MoeGroups g;
@@ -103,7 +120,8 @@ __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, &g_moe_gemm_fault_flags);
 }
 
-// A walk over the pair's tiles.
+// A walk over the pair's tiles, blocks of at most SLOTS slots.
+template <int SLOTS>
 struct TileWalk {
     int tile, e;            // current tile and its expert
     int slot0, slots, cols; // its slots, and their number rounded up to 16 (N)
@@ -118,7 +136,7 @@ struct TileWalk {
         if (tile >= sh.tile0[experts]) return false;
         while (tile >= sh.tile0[e + 1]) ++e;
         const int cnt = sh.count[e];
-        const int blocks = (cnt + kBlockSlots - 1) / kBlockSlots;
+        const int blocks = (cnt + SLOTS - 1) / SLOTS;
         const int local = tile - sh.tile0[e];
         row_tile = local / blocks;
         const int b = local - row_tile * blocks;
@@ -165,15 +183,17 @@ __device__ __forceinline__ void decode_group(const uint4 q0, const uint4 q1, flo
     }
 }
 
-template <bool SWIGLU>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMoeThreads, 1)
+template <bool SWIGLU, bool WIDE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MoeShape<WIDE>::threads, 1)
 q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
                     const __grid_constant__ CUtensorMap map_x, const MoeGemmParams p) {
+    using S = MoeShape<WIDE>;
+    constexpr int kBStages = S::b_stages, kWStages = S::w_stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* sb = smem;                                  // [stages][96][64] fp16, swizzled
-    uint8_t* sw = smem + kBStages * kBStageBytes;        // [stages][128][144]
+    uint8_t* sb = smem;                                  // [stages][2][slots / 2][64] fp16, swizzled
+    uint8_t* sw = smem + kBStages * S::b_stage;          // [stages][128][144]
     __shared__ MoeShared sh;
     volatile int* abort_flag = &sh.abort;
 
@@ -185,7 +205,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         sh.abort = 0;
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], 4 * kSets);        // decode warps
+            mbar_init(&sh.w_empty[i], 4 * S::sets);        // decode warps
         }
         for (int i = 0; i < kBStages; ++i) {
             mbar_init(&sh.full[i], 17);                  // B's bytes; two groups' decode warps in both CTAs
@@ -215,7 +235,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const int cnt = ok ? b - a : 0;
             sh.first[e] = a;
             sh.count[e] = cnt;
-            tiles = (cnt + kBlockSlots - 1) / kBlockSlots * p.row_tiles;
+            tiles = (cnt + S::slots - 1) / S::slots * p.row_tiles;
         }
         int scan = tiles;
 #pragma unroll
@@ -239,12 +259,12 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const uint32_t tmem = sh.tmem;
 
     if (warp < 4) {
-        regs_lower<kRegsCopy>();
+        regs_lower<S::regs_copy>();
         if (warp == 0) {
             // ------------------------------------------------ weight copies
             if (lane == 0) {
                 int it = 0;
-                TileWalk t;
+                TileWalk<S::slots> t;
                 for (t.start(); !*abort_flag && t.open(sh, experts); t.next()) {
                     const int per = SWIGLU ? 64 : kCtaRows;
                     const int row = t.e * p.n + (t.row_tile * 2 + static_cast<int>(rank)) * per;
@@ -271,18 +291,18 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             // pair's: its base address is 0.
             if (rank == 0) {
                 const int chunk = SWIGLU ? nsb : kPlainChunk;   // superblocks per accumulation
-                int s = 0, chunk_no = 0;     // B stage; accumulations so far
+                int s = 0, abuf = 0, chunk_no = 0;   // B stage, A buffer; accumulations so far
                 uint32_t par = 0;
                 bool ok = tmem == 0u;
                 const uint64_t desc0 = sw128_kmajor_desc(smem_addr(sb));
-                TileWalk t;
+                TileWalk<S::slots> t;
                 for (t.start(); ok && t.open(sh, experts); t.next()) {
                     const uint32_t idesc = mma_f16_idesc(256, t.cols);
                     for (int b = 0; ok && b < nsb; b += chunk, ++chunk_no) {
-                        const int dbuf = chunk_no & 1;
-                        if (chunk_no >= 2)
-                            ok = moe_wait(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / 2 - 1) & 1));
-                        const uint32_t dcol = static_cast<uint32_t>(dbuf * kBlockSlots);
+                        const int dbuf = chunk_no % S::d_bufs;
+                        if (chunk_no >= S::d_bufs)
+                            ok = moe_wait(&sh.d_empty[dbuf], static_cast<uint32_t>((chunk_no / S::d_bufs - 1) & 1));
+                        const uint32_t dcol = static_cast<uint32_t>(dbuf * S::slots);
                         const int steps = 2 * min(chunk, nsb - b);
 #pragma unroll 1
                         for (int i = 0; i < steps; ++i) {
@@ -290,12 +310,12 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                             if (!ok) break;
                             tc_fence_after_sync();
                             if (elect_one()) {
-                                const uint64_t bd = desc0 + static_cast<uint64_t>(s * (kBStageBytes >> 4));
-                                const uint32_t acol = kTmemA + (i & 1) * (kStep / 2);
+                                const uint64_t bd = desc0 + static_cast<uint64_t>(s * (S::b_stage >> 4));
+                                const uint32_t acol = S::a_col0 + abuf * (kStep / 2);
 #pragma unroll
                                 for (int kk = 0; kk < kStep / 16; ++kk)
                                     mma_f16_tmem_a_pair(dcol, acol + 8 * kk,
-                                                        bd + static_cast<uint64_t>((kk >> 2) * (kBHalfBytes >> 4) + 2 * (kk & 3)),
+                                                        bd + static_cast<uint64_t>((kk >> 2) * (S::b_half >> 4) + 2 * (kk & 3)),
                                                         idesc, i == 0 && kk == 0 ? 0u : 1u);
                                 mma_commit_pair(&sh.done[s]);
                                 if (i + 1 == steps) mma_commit_pair(&sh.d_full[dbuf]);
@@ -305,6 +325,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                                 s = 0;
                                 par ^= 1u;
                             }
+                            if (++abuf == S::a_bufs / 2) abuf = 0;
                         }
                     }
                 }
@@ -319,7 +340,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             int s = 0, it = 0;
             uint32_t par = 1;
             bool ok = true;
-            TileWalk t;
+            TileWalk<S::slots> t;
             const uint32_t bar0 = map_to_rank(&sh.full[0], 0);
             for (t.start(); ok && !*abort_flag && t.open(sh, experts); t.next()) {
                 const int half = t.cols / 2;
@@ -333,11 +354,11 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (elect_one()) {
                         if (rank == 0)   // both CTAs' bytes
                             mbar_arrive_expect_tx(&sh.full[s], 2u * 2u * boxes * kBBoxRows * kGroup * 2);
-                        uint8_t* dst = sb + s * kBStageBytes;
+                        uint8_t* dst = sb + s * S::b_stage;
                         for (int j = 0; j < boxes; ++j) {
                             tma_load_2d_pair(dst + j * kBBoxRows * kGroup * 2, &map_x, i * kStep, row + j * kBBoxRows,
                                              bar0 + 8 * s);
-                            tma_load_2d_pair(dst + kBHalfBytes + j * kBBoxRows * kGroup * 2, &map_x, i * kStep + kGroup,
+                            tma_load_2d_pair(dst + S::b_half + j * kBBoxRows * kGroup * 2, &map_x, i * kStep + kGroup,
                                              row + j * kBBoxRows, bar0 + 8 * s);
                         }
                     }
@@ -354,15 +375,15 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 for (int i = 0; i < 64; ++i) __nanosleep(1000000);
             }
         }
-    } else if (warp < kEpiWarp0) {
+    } else if (warp < S::epi_warp0) {
         // ---------------------------------------------------- decode
         // The pair's quant groups in the order of its tiles are numbered
-        // through: group i is decoded by set i % 3 into TMEM buffer i % 4 for
-        // step i / 2.
-        regs_lower<kRegsDecode>();
+        // through: group i is decoded by set i % sets into TMEM buffer i % a_bufs
+        // for step i / 2.
+        regs_lower<S::regs_decode>();
         const int quarter = warp & 3;
         const int row = SWIGLU ? (lane < 16 ? 0 : 64) + 16 * quarter + (lane & 15) : 32 * quarter + lane;
-        const uint32_t lane_addr = tmem + kTmemA + (static_cast<uint32_t>(32 * quarter) << 16);
+        const uint32_t lane_addr = tmem + S::a_col0 + (static_cast<uint32_t>(32 * quarter) << 16);
         const uint32_t full0 = map_to_rank(&sh.full[0], 0);
         const int pairs = static_cast<int>(gridDim.x >> 1), pair = static_cast<int>(blockIdx.x >> 1);
         const int tiles = sh.tile0[experts] > pair ? (sh.tile0[experts] - pair - 1) / pairs + 1 : 0;
@@ -371,7 +392,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         Header hd{};
         bool ok = true;
 #pragma unroll 1
-        for (uint32_t i = (warp - kDecodeWarp0) >> 2; i < groups; i += kSets) {
+        for (uint32_t i = (warp - kDecodeWarp0) >> 2; i < groups; i += S::sets) {
             const uint32_t b = i >> 2, g = i & 3u, ws = b % kWStages;
             const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
             if (b != have) {
@@ -388,17 +409,17 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             uint32_t r[32];
             decode_group(q0, q1, hd.d * small_u32_to_f32(scw & 0xFFu), hd.dmin * small_u32_to_f32(mw & 0xFFu),
                          hd.d * small_u32_to_f32((scw >> 8) & 0xFFu), hd.dmin * small_u32_to_f32((mw >> 8) & 0xFFu), r);
-            if ((i + kSets) >> 2 != b) {     // this warp's last group of the superblock
+            if ((i + S::sets) >> 2 != b) {     // this warp's last group of the superblock
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.w_empty[ws]);
             }
-            if (i >= kABufs) {               // the buffer's last step has been multiplied
-                const uint32_t step = (i - kABufs) >> 1;
+            if (i >= S::a_bufs) {               // the buffer's last step has been multiplied
+                const uint32_t step = (i - S::a_bufs) >> 1;
                 ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[step % kBStages], (step / kBStages) & 1u));
                 if (!ok) break;
                 tc_fence_after_sync();
             }
-            tmem_store_32cols(lane_addr + (i % kABufs) * (kGroup / 2), r);
+            tmem_store_32cols(lane_addr + (i % S::a_bufs) * (kGroup / 2), r);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
@@ -407,18 +428,17 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         if (!ok) *abort_flag = 1;
     } else {
         // ---------------------------------------------------- epilogue
-        regs_raise<kRegsEpi>();
-        const int quarter = warp & 3, part = (warp - kEpiWarp0) >> 2;
-        constexpr int kPart = kBlockSlots / 2;             // columns per warp
+        regs_raise<S::regs_epi>();
+        const int quarter = warp & 3, part = (warp - S::epi_warp0) >> 2;
+        constexpr int kPart = S::slots / 2;                // columns per warp
         const int c0 = part * kPart;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + c0;
         int chunk_no = 0;
         bool ok = true;
-        TileWalk t;
+        TileWalk<S::slots> t;
         for (t.start(); ok && t.open(sh, experts); t.next()) {
             // the pairs of this warp's columns, a column per lane and 32-column piece; -1: not stored
             int pair[kPart / 32];
-            uint32_t stored[kPart / 32];   // columns with one, as bits
 #pragma unroll
             for (int j = 0; j < kPart / 32; ++j) {
                 const int c = c0 + 32 * j + lane;
@@ -428,75 +448,65 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (v >= 0 && v < p.g.pairs) pair[j] = v;
                     else if (t.row_tile == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
                 }
-                stored[j] = __ballot_sync(0xFFFFFFFFu, pair[j] >= 0);
             }
-            if constexpr (SWIGLU) {
-                const int dbuf = chunk_no & 1;
-                ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / 2) & 1));
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    *abort_flag = 1;
-                    break;
-                }
+            float acc[kPart];
+            for (int b = 0; b < nsb; b += SWIGLU ? nsb : kPlainChunk) {
+                const int dbuf = chunk_no % S::d_bufs;
+                ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / S::d_bufs) & 1));
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
                 ++chunk_no;
                 tc_fence_after_sync();
+                // D into registers; from the second chunk on, added to them
+#pragma unroll
+                for (int j = 0; j < kPart / 8; ++j) {
+                    if (c0 + 8 * j < t.cols) {
+                        uint32_t r[8];
+                        tmem_load_8cols(lane_addr + dbuf * S::slots + 8 * j, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            acc[8 * j + c] = SWIGLU || b == 0 ? __uint_as_float(r[c]) : acc[8 * j + c] + __uint_as_float(r[c]);
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                break;
+            }
+            if constexpr (SWIGLU) {
                 const int feature = (t.row_tile * 2 + static_cast<int>(rank)) * 64 + 16 * quarter + (lane & 15);
                 const bool gate = lane < 16;
                 // lanes with gate rows finish even columns, lanes with up rows odd ones
                 __half* y = static_cast<__half*>(p.y) + static_cast<size_t>(t.slot0 + c0 + (gate ? 0 : 1)) * p.n + feature;
 #pragma unroll
                 for (int j = 0; j < kPart / 32; ++j) {
-                    if (c0 + 32 * j >= t.cols) break;
-                    uint32_t r[32];
-                    tmem_load_32cols(lane_addr + dbuf * kBlockSlots + 32 * j, r);
-                    const uint32_t mine = feature < p.n ? stored[j] >> (gate ? 0 : 1) : 0u;
+                    const uint32_t stored = __ballot_sync(0xFFFFFFFFu, pair[j] >= 0);
+                    const uint32_t mine = feature < p.n ? stored >> (gate ? 0 : 1) : 0u;
+                    if (stored == 0u) continue;
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, gate ? r[c + 1] : r[c], 16);
-                        const float gv = __uint_as_float(gate ? r[c] : other);
-                        const float uv = __uint_as_float(gate ? other : r[c + 1]);
+                        const float a = acc[32 * j + c], d = acc[32 * j + c + 1];
+                        const float other = __shfl_xor_sync(0xFFFFFFFFu, gate ? d : a, 16);
                         if (mine & (1u << c))
-                            y[static_cast<size_t>(32 * j + c) * p.n] = __float2half_rn(silu_mul_fast(gv, uv));
+                            y[static_cast<size_t>(32 * j + c) * p.n] =
+                                __float2half_rn(silu_mul_fast(gate ? a : other, gate ? other : d));
                     }
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
             } else {
-                float acc[kPart];
-#pragma unroll
-                for (int c = 0; c < kPart; ++c) acc[c] = 0.f;
-                for (int b = 0; b < nsb; b += kPlainChunk) {
-                    const int dbuf = chunk_no & 1;
-                    ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / 2) & 1));
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        *abort_flag = 1;
-                        break;
-                    }
-                    ++chunk_no;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int j = 0; j < kPart / 8; ++j) {
-                        if (c0 + 8 * j < t.cols) {
-                            uint32_t r[8];
-                            tmem_load_8cols(lane_addr + dbuf * kBlockSlots + 8 * j, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) acc[8 * j + c] += __uint_as_float(r[c]);
-                        }
-                    }
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
-                }
-                if (!ok) break;
                 const int row = (t.row_tile * 2 + static_cast<int>(rank)) * kCtaRows + 32 * quarter + lane;
                 float* y = static_cast<float*>(p.y) + row;
 #pragma unroll
-                for (int c = 0; c < kPart; ++c) {
-                    const int pr = __shfl_sync(0xFFFFFFFFu, pair[c / 32], c % 32);
-                    if (pr >= 0 && row < p.n) y[static_cast<size_t>(pr) * p.n] = acc[c];
+                for (int j = 0; j < kPart / 32; ++j) {
+                    if (__ballot_sync(0xFFFFFFFFu, pair[j] >= 0) == 0u) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int pr = __shfl_sync(0xFFFFFFFFu, pair[j], c);
+                        if (pr >= 0 && row < p.n) y[static_cast<size_t>(pr) * p.n] = acc[32 * j + c];
+                    }
                 }
             }
         }
@@ -644,11 +654,13 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
         p.nsb = nsb;
         const int tile_rows = swiglu ? kCtaRows : 2 * kCtaRows;
         p.row_tiles = (n + tile_rows - 1) / tile_rows;
+        const bool wide = g.pairs > static_cast<long long>(kNarrowPairsPerExpert) * g.experts;
         cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
-        cfg.blockDim = dim3(kMoeThreads);
-        cfg.dynamicSmemBytes = kMoeSmem;
-        e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<true>, mw, mw2, mx, p)
-                   : cudaLaunchKernelEx(&cfg, q4k_moe_gemm_kernel<false>, mw, mw2, mx, p);
+        cfg.blockDim = dim3(wide ? MoeShape<true>::threads : MoeShape<false>::threads);
+        cfg.dynamicSmemBytes = wide ? MoeShape<true>::smem : MoeShape<false>::smem;
+        auto* kernel = swiglu ? (wide ? q4k_moe_gemm_kernel<true, true> : q4k_moe_gemm_kernel<true, false>)
+                              : (wide ? q4k_moe_gemm_kernel<false, true> : q4k_moe_gemm_kernel<false, false>);
+        e = cudaLaunchKernelEx(&cfg, kernel, mw, mw2, mx, p);
     }
     if (work != nullptr) {
         const cudaError_t f = cudaFreeAsync(work, stream);
@@ -658,9 +670,11 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
 }
 
 int moe_gemm_set_attributes() {
-    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem);
+    constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, true>, attr, MoeShape<true>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, false>, attr, MoeShape<false>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, true>, attr, MoeShape<true>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, false>, attr, MoeShape<false>::smem);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 
