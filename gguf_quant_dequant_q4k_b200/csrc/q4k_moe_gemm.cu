@@ -116,7 +116,9 @@ struct MoeGemmParams {
     int n, nsb, row_tiles;
 };
 
+// A completed barrier passes in about 90 cycles (mbar_wait_bounded's loop: 160).
 __device__ __forceinline__ bool moe_wait(uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait_now(bar, parity)) return true;
     return mbar_wait_bounded(bar, parity, &g_moe_gemm_fault_flags);
 }
 
@@ -159,16 +161,52 @@ __device__ __forceinline__ float2 widen_half2(uint32_t bits) {
     return __half22float2(*reinterpret_cast<const __half2*>(&bits));
 }
 
-// The 64 weights of one quant group (two sub-blocks: low nibbles, high nibbles)
-// as 32 fp16 pairs in K order. A masked quant word is a pair of subnormal
-// binary16 values, q * 2^-24 (low nibbles) or q * 2^-20 (high nibbles), which
-// widen to f32 exactly; with 2^24 dsc0 and 2^20 dsc1 (exact) one fma gives the
-// weight dsc*q - dm rounded once, and cvt its binary16.
-__device__ __forceinline__ void decode_group(const uint4 q0, const uint4 q1, float dsc0, float dm0, float dsc1,
-                                             float dm1, uint32_t (&out)[32]) {
-    const float2 s0 = make_float2(dsc0 * 16777216.f, dsc0 * 16777216.f), c0 = make_float2(-dm0, -dm0);
-    const float2 s1 = make_float2(dsc1 * 1048576.f, dsc1 * 1048576.f), c1 = make_float2(-dm1, -dm1);
-    const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+// One quant group of a row on its way to fp16: 64 quants, and for its two
+// sub-blocks (low nibbles, high nibbles) the factor and the negated minimum.
+struct QuantGroup {
+    uint4 q0, q1;
+    float s0, c0, s1, c1;   // 2^24 d sc_2g, -dmin m_2g, 2^20 d sc_2g+1, -dmin m_2g+1
+};
+
+// A superblock header as the groups use it: the six-bit fields of a word become
+// f32 as binary16 subnormals (times 2^-24), so the powers of two go to d, dmin.
+struct GroupHeader {
+    uint32_t sc_lo, sc_hi, m_lo, m_hi;
+    float d48, d44, m24;    // 2^48 d, 2^44 d, -2^24 dmin (exact)
+
+    __device__ __forceinline__ void load(const uint8_t* src) {
+        const Header h = decode_header(*reinterpret_cast<const uint4*>(src));
+        sc_lo = h.sc_lo;
+        sc_hi = h.sc_hi;
+        m_lo = h.m_lo;
+        m_hi = h.m_hi;
+        d48 = h.d * 281474976710656.f;
+        d44 = h.d * 17592186044416.f;
+        m24 = h.dmin * -16777216.f;
+    }
+    __device__ __forceinline__ QuantGroup group(const uint8_t* src, uint32_t g) const {
+        QuantGroup r;
+        r.q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
+        r.q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
+        const uint32_t pick = (g & 1u) != 0u ? 0x4342u : 0x4140u;   // bytes 2 (g & 1) and the next, widened to 16 bits
+        const float2 sc = widen_half2(__byte_perm(g < 2 ? sc_lo : sc_hi, 0u, pick));
+        const float2 mn = widen_half2(__byte_perm(g < 2 ? m_lo : m_hi, 0u, pick));
+        r.s0 = d48 * sc.x;
+        r.s1 = d44 * sc.y;
+        r.c0 = m24 * mn.x;
+        r.c1 = m24 * mn.y;
+        return r;
+    }
+};
+
+// The group's 64 weights as 32 fp16 pairs in K order. A masked quant word is a
+// pair of subnormal binary16 values, q * 2^-24 (low nibbles) or q * 2^-20 (high
+// nibbles), which widen to f32 exactly; one fma gives the weight dsc*q - dm
+// rounded once, and cvt its binary16.
+__device__ __forceinline__ void decode_group(const QuantGroup& in, uint32_t (&out)[32]) {
+    const float2 s0 = make_float2(in.s0, in.s0), c0 = make_float2(in.c0, in.c0);
+    const float2 s1 = make_float2(in.s1, in.s1), c1 = make_float2(in.c1, in.c1);
+    const uint32_t w[8] = {in.q0.x, in.q0.y, in.q0.z, in.q0.w, in.q1.x, in.q1.y, in.q1.z, in.q1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t u = w[i] >> 8;
@@ -389,37 +427,43 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         const int tiles = sh.tile0[experts] > pair ? (sh.tile0[experts] - pair - 1) / pairs + 1 : 0;
         const uint32_t groups = 4u * static_cast<uint32_t>(tiles) * static_cast<uint32_t>(nsb);
         uint32_t have = ~0u;                 // superblock whose header is in hd
-        Header hd{};
+        GroupHeader hd{};
         bool ok = true;
-#pragma unroll 1
-        for (uint32_t i = (warp - kDecodeWarp0) >> 2; i < groups; i += S::sets) {
-            const uint32_t b = i >> 2, g = i & 3u, ws = b % kWStages;
+        auto fetch = [&](uint32_t i) {       // group i's quants and factors
+            const uint32_t b = i >> 2, ws = b % kWStages;
             const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
             if (b != have) {
                 ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], (b / kWStages) & 1u));
-                if (!ok) break;
-                hd = decode_header(*reinterpret_cast<const uint4*>(src));
+                if (!ok) return QuantGroup{};
+                hd.load(src);
                 have = b;
             }
-            const uint4 q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
-            const uint4 q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
-            // sub-blocks 2g and 2g + 1
-            const uint32_t scw = (g < 2 ? hd.sc_lo : hd.sc_hi) >> (16 * (g & 1));
-            const uint32_t mw = (g < 2 ? hd.m_lo : hd.m_hi) >> (16 * (g & 1));
-            uint32_t r[32];
-            decode_group(q0, q1, hd.d * small_u32_to_f32(scw & 0xFFu), hd.dmin * small_u32_to_f32(mw & 0xFFu),
-                         hd.d * small_u32_to_f32((scw >> 8) & 0xFFu), hd.dmin * small_u32_to_f32((mw >> 8) & 0xFFu), r);
-            if ((i + S::sets) >> 2 != b) {     // this warp's last group of the superblock
+            const QuantGroup q = hd.group(src, i & 3u);
+            if ((i + S::sets) >> 2 != b) {   // this warp's last group of the superblock
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.w_empty[ws]);
             }
-            if (i >= S::a_bufs) {               // the buffer's last step has been multiplied
-                const uint32_t step = (i - S::a_bufs) >> 1;
-                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.done[step % kBStages], (step / kBStages) & 1u));
+            return q;
+        };
+        uint32_t i = (warp - kDecodeWarp0) >> 2;
+        QuantGroup q{};
+        if (i < groups) q = fetch(i);
+#pragma unroll 1
+        for (; ok && i < groups; i += S::sets) {
+            // the buffer's last step: its barrier is polled ahead of the decoding, which covers the poll's latency
+            const uint32_t step = (i - S::a_bufs) >> 1;
+            uint64_t* free_bar = &sh.done[step % kBStages];
+            const uint32_t free_par = (step / kBStages) & 1u;
+            const bool free = i < S::a_bufs || mbar_try_wait_now(free_bar, free_par);
+            uint32_t r[32];
+            decode_group(q, r);
+            if (!__all_sync(0xFFFFFFFFu, free)) {
+                ok = __all_sync(0xFFFFFFFFu, moe_wait(free_bar, free_par));
                 if (!ok) break;
-                tc_fence_after_sync();
             }
+            tc_fence_after_sync();
             tmem_store_32cols(lane_addr + (i % S::a_bufs) * (kGroup / 2), r);
+            if (i + S::sets < groups) q = fetch(i + S::sets);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
