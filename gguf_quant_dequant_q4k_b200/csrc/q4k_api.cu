@@ -394,11 +394,11 @@ namespace {
 // w2 null for the plain forms), and the group description they launch with.
 int check_moe_product(const void* w, const void* w2, bool swiglu, const void* x, size_t xsize, const int* offsets,
                       const int* order, const void* y, size_t ysize, uintptr_t yalign, int n_experts, int n_pairs,
-                      int per_row, int n, int k, int max_pairs, MoeGroups* g) {
+                      int per_row, int n, int k, int max_k, int max_pairs, MoeGroups* g) {
     if (w == nullptr || (swiglu && w2 == nullptr) || offsets == nullptr) return Q4K_ERR_NULL;
     if (n_pairs > 0 && (x == nullptr || order == nullptr || y == nullptr)) return Q4K_ERR_NULL;
     const size_t wexpert = weight_bytes_checked(n, k);
-    if (wexpert == 0 || n_experts < 1 || n_experts > Q4K_MOE_MAX_EXPERTS || n_pairs < 0 || per_row < 0 ||
+    if (wexpert == 0 || k > max_k || n_experts < 1 || n_experts > Q4K_MOE_MAX_EXPERTS || n_pairs < 0 || per_row < 0 ||
         static_cast<long long>(n_experts) * n > INT32_MAX)
         return Q4K_ERR_SHAPE;
     if (n_pairs > max_pairs) return Q4K_ERR_UNSUPPORTED_M;
@@ -422,7 +422,7 @@ int moe_gemv(const void* w, const void* w2, bool swiglu, const float* x, const i
              int n_experts, int n_pairs, int per_row, int n, int k, q4k_stream_t stream) {
     MoeGroups g;
     int st = check_moe_product(w, w2, swiglu, x, 4, offsets, order, y, 4, 4, n_experts, n_pairs, per_row, n, k,
-                               Q4K_MOE_GEMV_MAX_PAIRS, &g);
+                               Q4K_MOE_GEMV_MAX_K, Q4K_MOE_GEMV_MAX_PAIRS, &g);
     if (st != Q4K_OK || n_pairs == 0) return st;
     DeviceInfo dev;
     st = current_device_info(&dev);
@@ -434,7 +434,7 @@ int moe_gemm(const void* w, const void* w2, bool swiglu, const void* x, const in
              int n_experts, int n_pairs, int per_row, int n, int k, q4k_stream_t stream) {
     MoeGroups g;
     int st = check_moe_product(w, w2, swiglu, x, 2, offsets, order, y, swiglu ? 2 : 4, swiglu ? 16 : 4, n_experts,
-                               n_pairs, per_row, n, k, INT32_MAX, &g);
+                               n_pairs, per_row, n, k, INT32_MAX, INT32_MAX, &g);
     if (st != Q4K_OK || n_pairs == 0) return st;
     DeviceInfo dev;
     st = current_device_info(&dev);

@@ -90,6 +90,7 @@ enum q4k_status {
 #define Q4K_MOE_MAX_EXPERTS 256 /* q4k_moe_*: most experts                       */
 #define Q4K_MOE_MAX_TOP_K 16    /* q4k_moe_route / q4k_moe_combine: most choices */
 #define Q4K_MOE_GEMV_MAX_PAIRS 4096 /* q4k_moe_gemv*: most pairs per call         */
+#define Q4K_MOE_GEMV_MAX_K 43008 /* q4k_moe_gemv*: longest rows                  */
 
 /*
  * y = W x for m vectors.
@@ -493,8 +494,11 @@ Q4K_API int q4k_moe_route(const float *logits, int *ids, float *weights, int *of
  * y[order[s]] = W_e x[row(s)] for every slot s of every expert e, in f32
  * (rows in pair order). n_pairs 0..Q4K_MOE_GEMV_MAX_PAIRS (more:
  * Q4K_ERR_UNSUPPORTED_M: that is q4k_moe_gemm_f16's size). K a positive
- * multiple of 256. y 4-byte aligned.
- * Accuracy: as q4k_gemv for the same row and matrix.
+ * multiple of 256 up to Q4K_MOE_GEMV_MAX_K (longer: Q4K_ERR_SHAPE). y 4-byte
+ * aligned.
+ * Accuracy: as q4k_gemv with two to four vectors on the integer kernel (x
+ * rounded to 2^-30 of its block's power of two, exact integer sums, one final
+ * rounding); an inf or NaN in a row of x makes that row's outputs NaN.
  * Returns a q4k_status.
  */
 Q4K_API int q4k_moe_gemv(const void *w, const float *x, const int *offsets, const int *order,

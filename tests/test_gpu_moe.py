@@ -187,7 +187,7 @@ GEMV_CASES = [  # tokens, experts, top_k, n, k, pad
     (1, 1, 1, 1, 256, 0), (1, 4, 2, 3, 512, 0), (2, 3, 1, 15, 768, 0), (3, 8, 2, 16, 1024, 0), (5, 4, 3, 17, 2048, 1),
     (1, 8, 8, 130, 1536, 0), (9, 4, 2, 257, 2304, 2), (24, 16, 4, 96, 1280, 3), (33, 2, 2, 64, 512, 0),
     (70, 3, 1, 40, 256, 5), (1, 8, 2, 1000, 4096, 0), (4, 8, 2, 300, 14336, 0), (2, 2, 1, 70, 20736, 0),
-    (16, 40, 6, 200, 1024, 1),
+    (16, 40, 6, 200, 1024, 1), (5, 2, 1, 17, 28672, 0), (4, 2, 1, 16, 43008, 0), (30, 3, 1, 1030, 2048, 0),
 ]
 
 

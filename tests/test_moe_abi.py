@@ -95,6 +95,7 @@ def test_gated_refusals(name):
 def test_gemv_refuses_prompt_sizes(name):
     big = 1 << 30
     assert product_status(name, n_pairs=q4k.Q4K_MOE_GEMV_MAX_PAIRS + 1, y=big) == q4k.Q4K_ERR_UNSUPPORTED_M
+    assert product_status(name, k=q4k.Q4K_MOE_GEMV_MAX_K + 256, y=big) == q4k.Q4K_ERR_SHAPE
 
 
 def combine_args(**kw):
