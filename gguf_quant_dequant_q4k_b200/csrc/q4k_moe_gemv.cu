@@ -23,14 +23,17 @@
 //   inside the sub-block that the digit image repeats). Rows 288 bytes apart
 //   make those 8-byte loads free of bank conflicts.
 // * Work. A unit is 16 rows x one group of vectors; clusters of CTAs own equal
-//   contiguous ranges of units, the CTAs of a cluster equal parts of K (so that
-//   the digit image of a part fits, and few long rows still fill the GPU), the
-//   warps of a CTA equal ranges of the (unit, box) items of a round of up to
-//   kRoundUnits units. Pieces of a unit meet in shared memory (the cluster's,
-//   through distributed shared memory) and are added in a fixed order.
+//   contiguous ranges of units, the CTAs of a cluster equal parts of K (one CTA
+//   where the digit image of the whole row fits), the warps of a CTA equal
+//   ranges of the (unit, box) items of a round. With one CTA per cluster a
+//   round is all its units of a group: a warp stores the units it has whole, and
+//   the units cut between warps (at most one per warp) meet in shared memory.
+//   With several, a round is up to kRoundUnits units and all pieces meet in the
+//   cluster's shared memory. Pieces are added in a fixed order.
 // * Bound: HBM for one and two vectors; the issue slots for four.
 #include <cstdint>
 #include <cuda.h>
+#include <mutex>
 #include <type_traits>
 
 #include "q4k_internal.h"
@@ -53,8 +56,13 @@ constexpr int kVBoxCols = 2;                      // superblocks per box
 constexpr int kVRowPitch = kVBoxCols * kBlockBytes;
 constexpr int kVBoxBytes = kVRows * kVRowPitch;
 constexpr int kVMaxVec = 4;                       // vectors per group
-constexpr int kRoundUnits = 16;
-constexpr int kVPieces = kRoundUnits + kVWarps;   // pieces of a round: unit + warp numbers them
+constexpr int kRoundUnits = 16;                   // most units of a round in a cluster of several CTAs
+// Pieces of units in shared memory. Several CTAs: every piece of a round,
+// numbered unit + warp (unique: of two neighbouring pieces one or both grow).
+// One CTA: a warp's first piece if it starts inside a unit (2 warp), its last if
+// it ends inside one (2 warp + 1).
+constexpr int kVPieces = 2 * kVWarps;
+static_assert(kRoundUnits + kVWarps <= kVPieces, "pieces of a round");
 constexpr int kVMaxCluster = 8;
 // Digit image of one superblock and two vectors: [sub-block pair][lane][2][8
 // bytes]; metadata per vector: 2^(E-30), from byte 16 l_0..7, from byte 48 h_0..7
@@ -63,11 +71,12 @@ constexpr int kVImageBytes = 2048;
 constexpr int kVMetaBytes = 80;
 __host__ __device__ constexpr int v_meta_offset(int cap) { return cap / 2 * kVImageBytes; }
 __host__ __device__ constexpr int v_sb_bytes(int cap) { return v_meta_offset(cap) + cap * kVMetaBytes; }
-__host__ __device__ constexpr int v_piece_doubles(bool swiglu) { return kVRows * kVMaxVec * (swiglu ? 2 : 1); }
+// [matrix][vector][row]
+__host__ __device__ constexpr int v_piece_doubles(int cap, bool swiglu) { return kVRows * cap * (swiglu ? 2 : 1); }
 // Shared memory of groups of up to `cap` vectors (4, or 2 for long K) and parts
 // of `sbs` superblocks; the most superblocks that fit.
 constexpr int v_smem(int sbs, int cap, bool swiglu) {
-    return 128 + kVWarps * kVStages * kVBoxBytes + sbs * v_sb_bytes(cap) + kVPieces * v_piece_doubles(swiglu) * 8;
+    return 128 + kVWarps * kVStages * kVBoxBytes + sbs * v_sb_bytes(cap) + kVPieces * v_piece_doubles(cap, swiglu) * 8;
 }
 constexpr int kVSmemLimit = 227 * 1024 - 4096;    // less the static part
 constexpr int v_max_sbs(int cap, bool swiglu) { return (kVSmemLimit - v_smem(0, cap, swiglu)) / v_sb_bytes(cap); }
@@ -299,10 +308,13 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         r.tile = static_cast<int>(u - static_cast<long long>(r.chunk) * p.units);
         while (r.chunk >= sh.chunk0[r.e + 1]) ++r.e;
         const long long left = min(u1 - u, static_cast<long long>(p.units - r.tile));
-        r.count = static_cast<int>(min(left, static_cast<long long>(kRoundUnits)));
+        r.count = static_cast<int>(csize > 1 ? min(left, static_cast<long long>(kRoundUnits)) : left);
         return r;
     };
-    auto item_begin = [&](int count, int w) { return count * boxes * w / kVWarps; };
+    auto item_begin = [&](int count, int w) {
+        return static_cast<int>(static_cast<long long>(count) * boxes * w / kVWarps);
+    };
+    const int piece = v_piece_doubles(p.cap, SWIGLU);
 
     // This warp's boxes in order, requested kVStages ahead of use.
     Round pr = open_round(u0, 0);
@@ -357,12 +369,29 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         }
         const int i0 = item_begin(r.count, warp), i1 = item_begin(r.count, warp + 1);
         bool ok = *static_cast<volatile int*>(&sh.abort) == 0;
+        // the group's pairs: vector v's in lane v (-1: not stored)
+        int my_pair = -1;
+        if (lane < vecs) {
+            const int v = __ldg(p.g.order + slot0 + lane);
+            if (v >= 0 && v < p.g.pairs) my_pair = v;
+            else if (warp == 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
+        }
+        // y of vector v's pair (v's own lane's, by shuffle) and a row of W
+        auto store = [&](int pair, int v, int grow, double a, double b) {
+            if (pair < 0 || grow >= p.n) return;
+            if constexpr (SWIGLU)
+                p.y[static_cast<size_t>(slot0 + v) * p.n + grow] = silu_mul(static_cast<float>(a), static_cast<float>(b));
+            else
+                p.y[static_cast<size_t>(pair) * p.n + grow] = static_cast<float>(a);
+        };
         auto run = [&](auto nt_tag) {
             constexpr int NT = decltype(nt_tag)::value;
             double acc[R][NT][2];
+            int unit = i0 / boxes, box = i0 - unit * boxes;
+            bool whole = true;       // the piece starts at its unit's first box
             for (int it = i0; it < i1 && ok; ++it) {
-                const int unit = it / boxes, box = it - unit * boxes;
                 if (it == i0 || box == 0) {
+                    whole = box == 0;
 #pragma unroll
                     for (int m = 0; m < R; ++m)
 #pragma unroll
@@ -386,22 +415,37 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         par ^= 1u;
                     }
                 }
-                if (it + 1 == i1 || box + 1 == boxes) {   // the piece of this unit
+                const bool ends = box + 1 == boxes;
+                if (ends || it + 1 == i1) {    // the piece of this unit
                     if (!parts_free) {
-                        if (csize > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
                         parts_free = true;
                     }
-                    double* out = parts + static_cast<size_t>(unit + warp) * v_piece_doubles(SWIGLU);
+                    const int t = lane & 3;
+                    double* out = parts + static_cast<size_t>(csize > 1 ? unit + warp : 2 * warp + (whole ? 1 : 0)) * piece;
+                    const int row = (lane >> 2) + 8 * (t & 1);      // even t takes rows 0..7, odd t rows 8..15
 #pragma unroll
-                    for (int m = 0; m < R; ++m)
+                    for (int i = 0; i < NT; ++i) {
+                        double v[2];
 #pragma unroll
-                        for (int i = 0; i < NT; ++i)
+                        for (int m = 0; m < R; ++m) {
+                            const double lo = acc[m][i][0] + __shfl_xor_sync(0xFFFFFFFFu, acc[m][i][0], 1);
+                            const double hi = acc[m][i][1] + __shfl_xor_sync(0xFFFFFFFFu, acc[m][i][1], 1);
+                            v[m] = (t & 1) ? hi : lo;
+                        }
+                        const int vec = 2 * i + (t >> 1);
+                        const int pair = __shfl_sync(0xFFFFFFFFu, my_pair, vec);
+                        if (csize == 1 && whole && ends) {
+                            store(pair, vec, (r.tile + unit) * kVRows + row, v[0], v[R - 1]);
+                        } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const double v = acc[m][i][h] + __shfl_xor_sync(0xFFFFFFFFu, acc[m][i][h], 1);
-                                if ((lane & 1) == 0)   // [matrix][vector][row]
-                                    out[(m * kVMaxVec + 2 * i + ((lane >> 1) & 1)) * kVRows + (lane >> 2) + 8 * h] = v;
-                            }
+                            for (int m = 0; m < R; ++m) out[(m * p.cap + vec) * kVRows + row] = v[m];
+                        }
+                    }
+                }
+                if (++box == boxes) {
+                    box = 0;
+                    ++unit;
                 }
             }
         };
@@ -409,55 +453,61 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         else run(std::integral_constant<int, 2>{});
         if (!ok) sh.abort = 1;
         if (!parts_free) {       // a warp without items in this round
-            if (csize > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
             parts_free = true;
         }
         __syncwarp();
         if (csize > 1) cluster_sync();
         else __syncthreads();
-        // Totals: thread = (unit, vector, row), the cluster's CTAs take alternate units; pieces in order of CTA and warp.
-        const int items = r.count * boxes;
-        for (int i = threadIdx.x; i < r.count * kVMaxVec * kVRows; i += kVThreads) {
-            const int unit = i / (kVMaxVec * kVRows), v = i / kVRows % kVMaxVec, row = i % kVRows;
-            if (unit % csize != rank || v >= vecs) continue;
-            const int grow = (r.tile + unit) * kVRows + row;
-            const int slot = slot0 + v, pair = __ldg(p.g.order + slot);
-            if (pair < 0 || pair >= p.g.pairs) {
-                atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
-                continue;
-            }
-            if (grow >= p.n) continue;
-            // the warps whose items touch the unit
-            const int wa = static_cast<int>((static_cast<long long>(unit * boxes + 1) * kVWarps - 1) / items);
-            const int wb = static_cast<int>((static_cast<long long>((unit + 1) * boxes) * kVWarps - 1) / items);
-            double sum[R];
-#pragma unroll
-            for (int m = 0; m < R; ++m) sum[m] = 0.0;
-            for (uint32_t cta = 0; cta < csize; ++cta)
-                for (int w = wa; w <= wb; ++w) {
-                    if (item_begin(r.count, w) == item_begin(r.count, w + 1)) continue;   // no items
+        const bool sound = *static_cast<volatile int*>(&sh.abort) == 0;
+        if (csize == 1) {
+            // Units cut between warps: warp w adds the unit its range starts inside, if no earlier warp's does: the
+            // tail of the warp before (with items), then the heads of w, w + 1, ...; lane = 16 (vector & 1) + row.
+            const int unit = i0 / boxes;
+            const int prev = i0 > 0 ? static_cast<int>((static_cast<long long>(i0) * kVWarps - 1) / (r.count * boxes)) : 0;
+            if (sound && i0 < i1 && i0 > unit * boxes && item_begin(r.count, prev) <= unit * boxes) {
+                const int row = lane & 15;
+                for (int v = lane >> 4; v - (lane >> 4) < vecs; v += 2) {
+                    double sum[2] = {0.0, 0.0};
 #pragma unroll
                     for (int m = 0; m < R; ++m) {
-                        const double* src = parts + static_cast<size_t>(unit + w) * v_piece_doubles(SWIGLU) +
-                                            (m * kVMaxVec + v) * kVRows + row;
-                        double d;
-                        if (csize == 1) d = *src;
-                        else asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(d) : "r"(map_to_rank(src, cta)) : "memory");
-                        sum[m] += d;
+                        const int at = (m * p.cap + v) * kVRows + row;
+                        double d = v < vecs ? parts[(2 * prev + 1) * piece + at] : 0.0;
+                        for (int w = warp; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
+                            if (v < vecs && item_begin(r.count, w) < item_begin(r.count, w + 1)) d += parts[2 * w * piece + at];
+                        sum[m] = d;
                     }
+                    const int pair = __shfl_sync(0xFFFFFFFFu, my_pair, v & 31);
+                    store(v < vecs ? pair : -1, v, (r.tile + unit) * kVRows + row, sum[0], sum[R - 1]);
                 }
-            if (sh.abort) continue;
-            if constexpr (SWIGLU)
-                p.y[static_cast<size_t>(slot) * p.n + grow] = silu_mul(static_cast<float>(sum[0]), static_cast<float>(sum[1]));
-            else
-                p.y[static_cast<size_t>(pair) * p.n + grow] = static_cast<float>(sum[0]);
-        }
-        __syncwarp();
-        if (csize > 1) {
+            }
+            __syncthreads();
+        } else {
+            // Totals: thread = (unit, vector, row), the cluster's CTAs take alternate units; pieces in order of CTA and warp.
+            const int items = r.count * boxes;
+            for (int i = threadIdx.x; i < r.count * p.cap * kVRows; i += kVThreads) {
+                const int unit = i / (p.cap * kVRows), v = i / kVRows % p.cap, row = i % kVRows;
+                if (unit % csize != rank || v >= vecs || !sound) continue;
+                const int pair = __ldg(p.g.order + slot0 + v);
+                // the warps whose items touch the unit
+                const int wa = ((unit * boxes + 1) * kVWarps - 1) / items, wb = ((unit + 1) * boxes * kVWarps - 1) / items;
+                double sum[2] = {0.0, 0.0};
+                for (uint32_t cta = 0; cta < csize; ++cta)
+                    for (int w = wa; w <= wb; ++w) {
+                        if (item_begin(r.count, w) == item_begin(r.count, w + 1)) continue;   // no items
+#pragma unroll
+                        for (int m = 0; m < R; ++m) {
+                            const double* src = parts + static_cast<size_t>(unit + w) * piece + (m * p.cap + v) * kVRows + row;
+                            double d;
+                            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(d) : "r"(map_to_rank(src, cta)) : "memory");
+                            sum[m] += d;
+                        }
+                    }
+                store(pair < p.g.pairs ? pair : -1, v, (r.tile + unit) * kVRows + row, sum[0], sum[R - 1]);
+            }
+            __syncwarp();
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
             parts_free = false;
-        } else {
-            __syncthreads();
         }
     }
     if (*static_cast<volatile int*>(&sh.abort) != 0)       // copies in flight land before shared memory goes
@@ -493,6 +543,36 @@ bool make_gemv_map(CUtensorMap* map, const void* w, long long rows, int nsb) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of csize CTAs that the current device holds at once: a cluster lies
+// in one GPC, so several SMs may stay without one, and a cluster more than fits
+// would run after all others.
+int gemv_clusters(int csize, int num_sms) {
+    if (csize == 1) return num_sms;
+    constexpr int kDevices = 64;
+    static std::once_flag once[kDevices];
+    static int fit[kDevices][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+    std::call_once(once[dev], [dev] {
+        for (int i = 1; i <= 3; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << i);
+            cfg.blockDim = dim3(kVThreads);
+            cfg.dynamicSmemBytes = kVSmemLimit;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&fit[dev][i], q4k_moe_gemv_kernel<true>, &cfg) != cudaSuccess) fit[dev][i] = 0;
+        }
+    });
+    const int got = fit[dev][csize == 2 ? 1 : csize == 4 ? 2 : 3];
+    return got < num_sms / csize ? got : num_sms / csize;
+}
+
 }  // namespace
 
 int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const float* x, const MoeGroups& g, float* y,
@@ -503,10 +583,14 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     CUtensorMap mw, mw2;
     if (!make_gemv_map(&mw, w, rows, nsb) || !make_gemv_map(&mw2, swiglu ? w2 : w, rows, nsb))
         return cuda_failure(cudaErrorInvalidValue);
-    // the smallest cluster whose CTAs' parts of K fit for groups of four vectors, else of two
-    int csize = 1, cap = kVMaxVec;
+    // Groups of up to four vectors, or of two where an expert has one pair on
+    // average (the image is half as large). The smallest cluster whose CTAs'
+    // parts of K fit (groups of two if none does).
+    int csize = 1, cap = g.pairs <= g.experts ? 2 : kVMaxVec;
     while (csize < kVMaxCluster && (nsb + csize - 1) / csize > v_max_sbs(cap, swiglu)) csize *= 2;
     if ((nsb + csize - 1) / csize > v_max_sbs(cap, swiglu)) cap = 2;
+    const int clusters = gemv_clusters(csize, dev.sm_count);
+    if (clusters <= 0) return cuda_failure(cudaErrorInvalidConfiguration);
     MoeGemvParams p{};
     p.g = g;
     p.x = x;
@@ -518,7 +602,7 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     p.part_sbs = (nsb + csize - 1) / csize;
     p.cap = cap;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / csize * csize));
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
     cfg.blockDim = dim3(kVThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(v_smem(p.part_sbs, cap, swiglu));
     cfg.stream = stream;

@@ -188,6 +188,7 @@ GEMV_CASES = [  # tokens, experts, top_k, n, k, pad
     (1, 8, 8, 130, 1536, 0), (9, 4, 2, 257, 2304, 2), (24, 16, 4, 96, 1280, 3), (33, 2, 2, 64, 512, 0),
     (70, 3, 1, 40, 256, 5), (1, 8, 2, 1000, 4096, 0), (4, 8, 2, 300, 14336, 0), (2, 2, 1, 70, 20736, 0),
     (16, 40, 6, 200, 1024, 1), (5, 2, 1, 17, 28672, 0), (4, 2, 1, 16, 43008, 0), (30, 3, 1, 1030, 2048, 0),
+    (1, 3, 1, 5, 1024, 0), (2, 6, 2, 2400, 1280, 0), (9, 2, 1, 5000, 512, 0), (3, 2, 2, 777, 4096, 0),
 ]
 
 
