@@ -7,11 +7,10 @@
 //   block b of a vector X = round(x * 2^(30 - E_b)), E_b the exponent of the
 //   block's largest |x|, in four balanced base-256 digits X = sum_l 256^l X_l.
 //   For every sub-block j the tensor cores form D_j[row][l] = sum q * X_l from
-//   the raw quants (unsigned bytes w & 0x0F0F0F0F; the high nibbles as 16 q),
-//   exact in 32 bits. P_l = sum_j sc_j D_j[l] and, with S0_j = sum of X over the
-//   sub-block, M = sum_j m_j S0_j are exact integers too, and the row's f64
-//   total gets 2^(E_b - 30) * (d * sum_l 256^l P_l - dmin * M); y is that total
-//   rounded once.
+//   the raw quants (unsigned bytes; the high nibbles in place, as 16 q), exact in
+//   32 bits, P_l = sum_j sc_j D_j[l], and with the digits' sums over the
+//   sub-blocks M_l = sum_j m_j sum X_l; the row's f64 total gets 2^(E_b - 30) *
+//   sum_l 256^l (d * P_l - dmin * M_l); y is that total rounded once.
 // * Tensor cores. mma.sync m16n8k32 (u8 x s8 -> s32): one MMA is 16 rows x one
 //   sub-block x the digits of two vectors. It issues 0.49 per cycle and SM
 //   (measured) against 0.16 that the HBM rate needs for two vectors; unlike
@@ -59,14 +58,13 @@ constexpr int kVMaxVec = 4;                       // vectors per group
 constexpr int kRoundUnits = 16;                   // most units of a round in a cluster of several CTAs
 // Pieces of units in shared memory. Several CTAs: every piece of a round,
 // numbered unit + warp (unique: of two neighbouring pieces one or both grow).
-// One CTA: a warp's first piece if it starts inside a unit (2 warp), its last if
-// it ends inside one (2 warp + 1).
-constexpr int kVPieces = 2 * kVWarps;
-static_assert(kRoundUnits + kVWarps <= kVPieces, "pieces of a round");
+// One CTA: a warp's first piece if it starts inside a unit (its head), which the
+// warp with the unit's first boxes adds when it comes to its own range's end.
+__host__ __device__ constexpr int v_pieces(bool one_cta) { return one_cta ? kVWarps : kRoundUnits + kVWarps; }
 constexpr int kVMaxCluster = 8;
 // Digit image of one superblock and two vectors: [sub-block pair][lane][2][8
-// bytes]; metadata per vector: 2^(E-30), from byte 16 l_0..7, from byte 48 h_0..7
-// with S0_j = 2^18 h_j + l_j.
+// bytes]; behind the images per vector 2^(E-30), and from byte 16 the sums of
+// each digit over the sub-blocks, 16 bits each: [digit][sub-block].
 constexpr int kVImageBytes = 2048;
 constexpr int kVMetaBytes = 80;
 __host__ __device__ constexpr int v_meta_offset(int cap) { return cap / 2 * kVImageBytes; }
@@ -75,12 +73,15 @@ __host__ __device__ constexpr int v_sb_bytes(int cap) { return v_meta_offset(cap
 __host__ __device__ constexpr int v_piece_doubles(int cap, bool swiglu) { return kVRows * cap * (swiglu ? 2 : 1); }
 // Shared memory of groups of up to `cap` vectors (4, or 2 for long K) and parts
 // of `sbs` superblocks; the most superblocks that fit.
-constexpr int v_smem(int sbs, int cap, bool swiglu) {
-    return 128 + kVWarps * kVStages * kVBoxBytes + sbs * v_sb_bytes(cap) + kVPieces * v_piece_doubles(cap, swiglu) * 8;
+constexpr int v_smem(int sbs, int cap, bool swiglu, bool one_cta) {
+    return 128 + kVWarps * kVStages * kVBoxBytes + sbs * v_sb_bytes(cap) +
+           v_pieces(one_cta) * v_piece_doubles(cap, swiglu) * 8;
 }
-constexpr int kVSmemLimit = 227 * 1024 - 4096;    // less the static part
-constexpr int v_max_sbs(int cap, bool swiglu) { return (kVSmemLimit - v_smem(0, cap, swiglu)) / v_sb_bytes(cap); }
-static_assert(v_max_sbs(2, true) * kVMaxCluster * kQK >= Q4K_MOE_GEMV_MAX_K, "every accepted K fits");
+constexpr int kVSmemLimit = 227 * 1024 - 6144;    // less the static part
+constexpr int v_max_sbs(int cap, bool swiglu, bool one_cta) {
+    return (kVSmemLimit - v_smem(0, cap, swiglu, one_cta)) / v_sb_bytes(cap);
+}
+static_assert(v_max_sbs(2, true, false) * kVMaxCluster * kQK >= Q4K_MOE_GEMV_MAX_K, "every accepted K fits");
 
 struct MoeGemvParams {
     MoeGroups g;
@@ -92,13 +93,18 @@ struct MoeGemvParams {
     int cap;        // most vectors per group: 4 or 2
 };
 
-struct GemvShared {
+struct GemvShared {   // static: below the 6 KB that kVSmemLimit leaves
     uint64_t full[kVWarps][kVStages];
-    int warp_sum[kVWarps];
     int chunk0[Q4K_MOE_MAX_EXPERTS + 1];            // first vector group of each expert
     int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];
+    int order[kVThreads];                           // of the first pairs
+    long long range[2];
+    int head[kVWarps];                              // rounds whose head piece the warp has left, plus one
     int abort;
 };
+
+// d = A B^T: A 16 x 32 unsigned bytes (a0, a2: row g, a1, a3: row g + 8), B 8 x 32 signed.
+static_assert(sizeof(GemvShared) <= 6144 - 256, "shared memory");
 
 __device__ __forceinline__ void imma(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
@@ -108,67 +114,74 @@ __device__ __forceinline__ void imma(int (&d)[4], uint32_t a0, uint32_t a1, uint
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 
+// c + the products of the two signed 16-bit halves of a with bytes 0, 1 (lo) or
+// 2, 3 (hi) of b.
+__device__ __forceinline__ int dp2a_lo(int a, uint32_t b, int c) {
+    int d;
+    asm("dp2a.lo.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ int dp2a_hi(int a, uint32_t b, int c) {
+    int d;
+    asm("dp2a.hi.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 // A 32-bit integer as f64, exactly: 2^52 + 2^31 + v less 2^52 + 2^31.
 __device__ __forceinline__ double int_to_f64(int v) {
     return __hiloint2double(0x43300000, v ^ static_cast<int>(0x80000000u)) - 4503601774854144.0;
 }
 
-// The digits of one vector's block: lane holds K positions 8 lane .. + 7.
-__device__ __forceinline__ void block_digits(const float* __restrict__ x, int vec, uint8_t* sb_image, int meta_offset,
-                                             int lane) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(x) + 2 * lane);
-    const float4 c = __ldg(reinterpret_cast<const float4*>(x) + 2 * lane + 1);
-    const float v[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-    bool finite = true;
-    float amax = 0.f;
+// The digits of one vector's block (lane: K positions 8 lane .. + 7, v). E is
+// taken from the exponent field of the largest |x| (-125 at least).
+__device__ __forceinline__ void block_digits(const float (&v)[8], int vec, uint8_t* sb_image, int meta_offset, int lane) {
+    uint32_t top = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        finite = finite && isfinite(v[e]);
-        amax = fmaxf(amax, fabsf(v[e]));
-    }
-    finite = __all_sync(0xFFFFFFFFu, finite);
-    amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));   // non-negative: ordered as integers
-    const bool scaled = finite && amax > 0.f;
-    int ex = 0;
-    if (scaled) frexpf(amax, &ex);                       // amax in [2^(ex-1), 2^ex)
-    const double up = scaled ? __longlong_as_double(static_cast<long long>(1023 + 30 - ex) << 52) : 0.0;
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);             // non-negative floats are ordered as integers
+    const bool finite = top < 0x7F800000u;
+    const int ex = max(static_cast<int>(top >> 23), 1) - 126;   // |x| < 2^ex
+    // x 2^(30 - ex) in two exact steps (the power may lie outside f32; a step that underflows belongs to a digit 0)
+    const int s1 = (30 - ex) / 2, s2 = 30 - ex - s1;
+    const float up1 = __int_as_float((127 + s1) << 23), up2 = __int_as_float((127 + s2) << 23);
     int r[8];
-    long long sum = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        r[e] = scaled ? __double2int_rn(static_cast<double>(v[e]) * up) : 0;
-        sum += r[e];
-    }
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);         // S0 of sub-block j: lanes 4j .. 4j + 3
-    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-    uint8_t* meta = sb_image + meta_offset + vec * kVMetaBytes;
+    for (int e = 0; e < 8; ++e) r[e] = finite ? __float2int_rn(v[e] * up1 * up2) : 0;
     const int j = lane >> 2, t = lane & 3;
-    if (t == 0) {
-        reinterpret_cast<int*>(meta + 16)[j] = static_cast<int>(sum & 0x3FFFF);
-        reinterpret_cast<int*>(meta + 48)[j] = static_cast<int>(sum >> 18);
-    }
     if (lane == 0)
-        *reinterpret_cast<double*>(meta) =
-            finite ? (scaled ? __longlong_as_double(static_cast<long long>(1023 + ex - 30) << 52) : 0.0)
-                   : __longlong_as_double(0x7FF8000000000000LL);
-    uint8_t* img = sb_image + (vec >> 1) * kVImageBytes + (j >> 1) * 512 + (j & 1) * 8;
+        *reinterpret_cast<double*>(sb_image + meta_offset + vec * kVMetaBytes) =
+            __longlong_as_double(finite ? static_cast<long long>(1023 + ex - 30) << 52 : 0x7FF8000000000000LL);
+    // With 128 (1 + 256 + 256^2) added, the lower three bytes are the balanced digits plus 128: flipping their top
+    // bits leaves the four signed digits as bytes. Then bytes l of four elements are brought together.
+    uint32_t z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = (static_cast<uint32_t>(r[e]) + 0x00808080u) ^ 0x00808080u;
+    uint8_t* img = sb_image + (vec >> 1) * kVImageBytes + (j >> 1) * 512 + (j & 1) * 8 + (16 * (vec & 1) + t) * 16;
+    uint32_t w[4][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t lo01 = __byte_perm(z[4 * h], z[4 * h + 1], 0x5140), hi01 = __byte_perm(z[4 * h], z[4 * h + 1], 0x7362);
+        const uint32_t lo23 = __byte_perm(z[4 * h + 2], z[4 * h + 3], 0x5140);
+        const uint32_t hi23 = __byte_perm(z[4 * h + 2], z[4 * h + 3], 0x7362);
+        w[0][h] = __byte_perm(lo01, lo23, 0x5410);
+        w[1][h] = __byte_perm(lo01, lo23, 0x7632);
+        w[2][h] = __byte_perm(hi01, hi23, 0x5410);
+        w[3][h] = __byte_perm(hi01, hi23, 0x7632);
+    }
 #pragma unroll
     for (int l = 0; l < 4; ++l) {
-        uint32_t w[2] = {0u, 0u};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int dig = l < 3 ? ((r[e] + 128) & 255) - 128 : r[e];
-            r[e] = (r[e] - dig) >> 8;
-            w[e >> 2] |= (static_cast<uint32_t>(dig) & 0xFFu) << (8 * (e & 3));
-        }
-        const int col = 4 * (vec & 1) + l;
-        *reinterpret_cast<uint2*>(img + (4 * col + t) * 16) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(img + l * 64) = make_uint2(w[l][0], w[l][1]);
+        int sum = __dp4a(static_cast<int>(w[l][0]), 0x01010101, __dp4a(static_cast<int>(w[l][1]), 0x01010101, 0));
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);        // sub-block j: lanes 4j .. 4j + 3
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        if (t == l)
+            reinterpret_cast<int16_t*>(sb_image + meta_offset + vec * kVMetaBytes + 16)[8 * l + j] = static_cast<int16_t>(sum);
     }
 }
 
 // Adds one superblock of 16 rows to the lane's totals: acc[nt][0] for row g,
-// acc[nt][1] for row g + 8, each the lane's two digit columns of vector 2 nt +
-// t / 2 (digits 0, 1 for even t, 2, 3 for odd t) and its half of the M term.
+// acc[nt][1] for row g + 8, each over the lane's two digits of vector 2 nt +
+// t / 2 (digits 0, 1 for even t; 2, 3, in units of 256^2, for odd t).
 template <int NT>
 __device__ __forceinline__ void superblock_rows(const uint8_t* rows, const uint8_t* sb_image, int meta_offset, int lane,
                                                 double (&acc)[NT][2]) {
@@ -177,54 +190,52 @@ __device__ __forceinline__ void superblock_rows(const uint8_t* rows, const uint8
     const uint8_t* rb = ra + 8 * kVRowPitch;
     const Header ha = decode_header(*reinterpret_cast<const uint4*>(ra));
     const Header hb = decode_header(*reinterpret_cast<const uint4*>(rb));
-    int pe[NT][4], po[NT][4];
+    int ps[NT][4];      // 16 P_l: even sub-blocks with 16 sc_j, odd ones with 16 q (the high nibbles in place)
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) pe[i][c] = po[i][c] = 0;
+        for (int c = 0; c < 4; ++c) ps[i][c] = 0;
 #pragma unroll
     for (int jp = 0; jp < 4; ++jp) {
         const uint2 qa = *reinterpret_cast<const uint2*>(ra + kQsOffset + 32 * jp + 8 * t);
         const uint2 qb = *reinterpret_cast<const uint2*>(rb + kQsOffset + 32 * jp + 8 * t);
         const uint32_t wa = jp < 2 ? ha.sc_lo : ha.sc_hi, wb = jp < 2 ? hb.sc_lo : hb.sc_hi;
-        const int sae = static_cast<int>(byte_of(wa, (2 * jp) & 3)), sao = static_cast<int>(byte_of(wa, (2 * jp + 1) & 3));
-        const int sbe = static_cast<int>(byte_of(wb, (2 * jp) & 3)), sbo = static_cast<int>(byte_of(wb, (2 * jp + 1) & 3));
+        const int sae = static_cast<int>(16u * byte_of(wa, (2 * jp) & 3)), sao = static_cast<int>(byte_of(wa, (2 * jp + 1) & 3));
+        const int sbe = static_cast<int>(16u * byte_of(wb, (2 * jp) & 3)), sbo = static_cast<int>(byte_of(wb, (2 * jp + 1) & 3));
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const uint4 dg = *reinterpret_cast<const uint4*>(sb_image + i * kVImageBytes + jp * 512 + lane * 16);
             int d[4];
             imma(d, qa.x & 0x0F0F0F0Fu, qb.x & 0x0F0F0F0Fu, qa.y & 0x0F0F0F0Fu, qb.y & 0x0F0F0F0Fu, dg.x, dg.y);
-            pe[i][0] += sae * d[0];
-            pe[i][1] += sae * d[1];
-            pe[i][2] += sbe * d[2];
-            pe[i][3] += sbe * d[3];
+            ps[i][0] += sae * d[0];
+            ps[i][1] += sae * d[1];
+            ps[i][2] += sbe * d[2];
+            ps[i][3] += sbe * d[3];
             imma(d, qa.x & 0xF0F0F0F0u, qb.x & 0xF0F0F0F0u, qa.y & 0xF0F0F0F0u, qb.y & 0xF0F0F0F0u, dg.z, dg.w);
-            po[i][0] += sao * d[0];    // sixteen times the sums
-            po[i][1] += sao * d[1];
-            po[i][2] += sbo * d[2];
-            po[i][3] += sbo * d[3];
+            ps[i][0] += sao * d[0];
+            ps[i][1] += sao * d[1];
+            ps[i][2] += sbo * d[2];
+            ps[i][3] += sbo * d[3];
         }
     }
-    const bool low = (t & 1) == 0;
-    const double fs = low ? 1.0 : 65536.0, fm = low ? -1.0 : -262144.0;
-    const double da = ha.d * fs, db = hb.d * fs, ma = ha.dmin * fm, mb = hb.dmin * fm;
+    const double da = ha.d * 0.0625f, db = hb.d * 0.0625f, ma = -ha.dmin, mb = -hb.dmin;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const uint8_t* meta = sb_image + meta_offset + (2 * i + (t >> 1)) * kVMetaBytes;
-        const int4 x0 = *reinterpret_cast<const int4*>(meta + (low ? 16 : 48));
-        const int4 x1 = *reinterpret_cast<const int4*>(meta + (low ? 16 : 48) + 16);
-        const int xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        int sa = 0, sb = 0;            // |m l| sums < 8 * 63 * 2^18, |m h| sums < 8 * 63 * 2^17
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            sa += static_cast<int>(byte_of(j < 4 ? ha.m_lo : ha.m_hi, j & 3)) * xs[j];
-            sb += static_cast<int>(byte_of(j < 4 ? hb.m_lo : hb.m_hi, j & 3)) * xs[j];
-        }
         const double scale = *reinterpret_cast<const double*>(meta);
-        const double pa = fma(256.0, int_to_f64(pe[i][1] + (po[i][1] >> 4)), int_to_f64(pe[i][0] + (po[i][0] >> 4)));
-        const double pb = fma(256.0, int_to_f64(pe[i][3] + (po[i][3] >> 4)), int_to_f64(pe[i][2] + (po[i][2] >> 4)));
-        acc[i][0] = fma(scale, fma(da, pa, ma * int_to_f64(sa)), acc[i][0]);
-        acc[i][1] = fma(scale, fma(db, pb, mb * int_to_f64(sb)), acc[i][1]);
+        const int4 s0 = *reinterpret_cast<const int4*>(meta + 16 + 32 * (t & 1));        // the lane's lower digit
+        const int4 s1 = *reinterpret_cast<const int4*>(meta + 16 + 32 * (t & 1) + 16);
+        // M of two digits: |M_l| <= 8 * 63 * 4096, so M_0 + 256 M_1 fits 32 bits
+        auto mins = [](const int4& s, uint32_t lo, uint32_t hi) {
+            return dp2a_lo(s.x, lo, dp2a_hi(s.y, lo, dp2a_lo(s.z, hi, dp2a_hi(s.w, hi, 0))));
+        };
+        const int m_a = mins(s0, ha.m_lo, ha.m_hi) + 256 * mins(s1, ha.m_lo, ha.m_hi);
+        const int m_b = mins(s0, hb.m_lo, hb.m_hi) + 256 * mins(s1, hb.m_lo, hb.m_hi);
+        // |16 P_l| <= 16 * 8 * 63 * 32 * 15 * 128 < 2^29
+        const double pa = fma(256.0, int_to_f64(ps[i][1]), int_to_f64(ps[i][0]));
+        const double pb = fma(256.0, int_to_f64(ps[i][3]), int_to_f64(ps[i][2]));
+        acc[i][0] = fma(scale, fma(da, pa, ma * int_to_f64(m_a)), acc[i][0]);
+        acc[i][1] = fma(scale, fma(db, pb, mb * int_to_f64(m_b)), acc[i][1]);
     }
 }
 
@@ -253,8 +264,10 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const int sbs = max(0, min(p.part_sbs, p.nsb - sb0));  // this CTA's superblocks
     const int boxes = (p.part_sbs + kVBoxCols - 1) / kVBoxCols;   // per unit and matrix, the same in every CTA
 
-    if (lane == 0)
+    if (lane == 0) {
         for (int s = 0; s < kVStages; ++s) mbar_init(&sh.full[warp][s], 1);
+        sh.head[warp] = 0;
+    }
     if (threadIdx.x == 0) {
         sh.abort = 0;
         tma_prefetch_map(&map_w);
@@ -263,37 +276,41 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     fence_mbar_init();
     pdl_launch_dependents();
     pdl_wait();
-    // Experts' slots and first vector groups.
-    {
-        const int e = threadIdx.x;
-        int chunks = 0;
-        if (e < experts) {
-            const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
-            const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
-            if (!ok && blockIdx.x == 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
-            const int cnt = ok ? b - a : 0;
-            sh.first[e] = a;
-            sh.count[e] = cnt;
-            chunks = (cnt + p.cap - 1) / p.cap;
-        }
-        int scan = chunks;
+    // Experts' slots and first vector groups (warp 0; the others' redundant scans would fill the issue slots).
+    if (threadIdx.x < p.g.pairs) sh.order[threadIdx.x] = __ldg(p.g.order + threadIdx.x);
+    if (warp == 0) {
+        int before = 0;
+        for (int e0 = 0; e0 < experts; e0 += 32) {
+            const int e = e0 + lane;
+            int chunks = 0;
+            if (e < experts) {
+                const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
+                const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
+                if (!ok && blockIdx.x == 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
+                const int cnt = ok ? b - a : 0;
+                sh.first[e] = a;
+                sh.count[e] = cnt;
+                chunks = (cnt + p.cap - 1) >> (p.cap == 4 ? 2 : 1);
+            }
+            int scan = chunks;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
-            if (lane >= off) scan += v;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
+                if (lane >= off) scan += v;
+            }
+            if (e < experts) sh.chunk0[e + 1] = before + scan;
+            before += __shfl_sync(0xFFFFFFFFu, scan, 31);
         }
-        if (lane == 31) sh.warp_sum[warp] = scan;
-        __syncthreads();
-        if (e < experts) {
-            int before = 0;
-            for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-            sh.chunk0[e + 1] = before + scan;
-            if (e == 0) sh.chunk0[0] = 0;
+        if (lane < 2) {              // this cluster's units: [range[0], range[1])
+            const long long all = static_cast<long long>(before) * p.units;
+            sh.range[lane] = all < (1 << 23)   // at most 148 clusters: 32-bit division
+                                 ? static_cast<long long>(static_cast<uint32_t>(all) * (cid + lane) / nclusters)
+                                 : all * (cid + lane) / nclusters;
         }
-        __syncthreads();
+        if (lane == 0) sh.chunk0[0] = 0;
     }
-    const long long total = static_cast<long long>(sh.chunk0[experts]) * p.units;
-    const long long u0 = total * cid / nclusters, u1 = total * (cid + 1) / nclusters;
+    __syncthreads();
+    const long long u0 = sh.range[0], u1 = sh.range[1];
 
     // The rounds of this cluster: up to kRoundUnits units of one vector group.
     struct Round {
@@ -304,7 +321,8 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     auto open_round = [&](long long u, int e) {
         Round r{u, 0, e, 0, 0};
         if (u >= u1) return r;
-        r.chunk = static_cast<int>(u / p.units);
+        r.chunk = u1 < (1 << 23) ? static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(p.units))
+                                    : static_cast<int>(u / p.units);
         r.tile = static_cast<int>(u - static_cast<long long>(r.chunk) * p.units);
         while (r.chunk >= sh.chunk0[r.e + 1]) ++r.e;
         const long long left = min(u1 - u, static_cast<long long>(p.units - r.tile));
@@ -312,70 +330,128 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         return r;
     };
     auto item_begin = [&](int count, int w) {
-        return static_cast<int>(static_cast<long long>(count) * boxes * w / kVWarps);
+        return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(count) * static_cast<uint32_t>(boxes)) *
+                                static_cast<uint32_t>(w) / kVWarps);
     };
     const int piece = v_piece_doubles(p.cap, SWIGLU);
 
     // This warp's boxes in order, requested kVStages ahead of use.
-    Round pr = open_round(u0, 0);
-    int p_item = item_begin(pr.count, warp), p_mat = 0, p_stage = 0;
+    const Round first_round = open_round(u0, 0);
+    Round pr = first_round;
+    int p_left = 0, p_box = 0, p_row = 0, p_mat = 0, p_stage = 0;   // items left in the round, the next one's box and row
+    auto enter = [&] {
+        const int i0 = item_begin(pr.count, warp);
+        p_left = item_begin(pr.count, warp + 1) - i0;
+        const int unit = i0 / boxes;
+        p_box = i0 - unit * boxes;
+        p_row = pr.e * p.n + (pr.tile + unit) * kVRows;
+    };
+    enter();
     auto request = [&] {
-        while (pr.count > 0 && p_item >= item_begin(pr.count, warp + 1)) {
+        while (p_left == 0) {
+            if (pr.count == 0) return;
             pr = open_round(pr.u + pr.count, pr.e);
-            p_item = item_begin(pr.count, warp);
+            enter();
         }
-        if (pr.count == 0) return;
         if (lane == 0) {
-            const int unit = p_item / boxes, box = p_item - unit * boxes;
             mbar_arrive_expect_tx(&sh.full[warp][p_stage], kVBoxBytes);
             tma_load_3d(ring + (warp * kVStages + p_stage) * kVBoxBytes, p_mat == 0 ? &map_w : &map_w2, 0,
-                        sb0 + box * kVBoxCols, pr.e * p.n + (pr.tile + unit) * kVRows, &sh.full[warp][p_stage]);
+                        sb0 + p_box * kVBoxCols, p_row, &sh.full[warp][p_stage]);
         }
         if (++p_mat == R) {
             p_mat = 0;
-            ++p_item;
+            --p_left;
+            if (++p_box == boxes) {
+                p_box = 0;
+                p_row += kVRows;
+            }
         }
         p_stage = (p_stage + 1) % kVStages;
     };
-    for (int s = 0; s < kVStages; ++s) request();
+
+    // A round's vector group: its slots, and vector v's pair in lane v (-1: not stored).
+    struct Group {
+        int slot0, vecs, pair;
+    };
+    auto open_group = [&](const Round& r) {
+        const int cnt = sh.count[r.e], chunks = sh.chunk0[r.e + 1] - sh.chunk0[r.e], c = r.chunk - sh.chunk0[r.e];
+        int v0 = 0, v1 = cnt;        // an expert's vectors in equal groups
+        if (chunks > 1) {
+            v0 = static_cast<int>(static_cast<uint32_t>(cnt) * static_cast<uint32_t>(c) / static_cast<uint32_t>(chunks));
+            v1 = static_cast<int>(static_cast<uint32_t>(cnt) * static_cast<uint32_t>(c + 1) / static_cast<uint32_t>(chunks));
+        }
+        Group g;
+        g.vecs = v1 - v0;
+        g.slot0 = sh.first[r.e] + v0;
+        g.pair = -1;
+        if (lane < g.vecs) {
+            const int slot = g.slot0 + lane;
+            const int v = slot < kVThreads ? sh.order[slot] : __ldg(p.g.order + slot);
+            if (v >= 0 && v < p.g.pairs) g.pair = v;
+        }
+        return g;
+    };
+    // Block `job` = (superblock, vector) of the group's digit image: this lane's eight elements.
+    auto block_of = [](int job, int vecs) { return vecs == 3 ? job * 43691 >> 17 : job >> (vecs >> 1); };   // job / vecs
+    auto fetch = [&](const Group& g, int job, float (&v)[8]) {
+        const int b = block_of(job, g.vecs), vec = job - b * g.vecs;
+        const int pair = __shfl_sync(0xFFFFFFFFu, g.pair, vec);
+        const int row = p.g.per_row == 0 ? g.slot0 + vec : pair >= 0 ? pair / p.g.per_row : 0;
+        const float4* src =
+            reinterpret_cast<const float4*>(p.x + static_cast<size_t>(row) * p.k + static_cast<size_t>(sb0 + b) * kQK) + 2 * lane;
+        const float4 lo = __ldg(src), hi = __ldg(src + 1);
+        v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+        v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    };
 
     int stage = 0;
     uint32_t par = 0;
     int chunk_of_image = -1;
     bool parts_free = true;      // no CTA still reads this one's pieces
-    for (Round r = open_round(u0, 0); r.count > 0; r = open_round(r.u + r.count, r.e)) {
-        const int cnt = sh.count[r.e], chunks = sh.chunk0[r.e + 1] - sh.chunk0[r.e], c = r.chunk - sh.chunk0[r.e];
-        const int v0 = static_cast<int>(static_cast<long long>(cnt) * c / chunks);
-        const int vecs = static_cast<int>(static_cast<long long>(cnt) * (c + 1) / chunks) - v0;
-        const int slot0 = sh.first[r.e] + v0;
+    int round_no = 0;
+    // A warp's head piece of a round is in shared memory (its writes released, acquired by the reader).
+    auto publish_head = [&](int round) {
+        asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_addr(&sh.head[warp])), "r"(round + 1) : "memory");
+    };
+    auto wait_head = [&](int w, int round) {
+        for (unsigned i = 0; i < kSpinLimit; ++i) {
+            int v;
+            asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(&sh.head[w])) : "memory");
+            if (v == round + 1) return true;
+            __nanosleep(64);
+        }
+        atomicOr(&g_moe_gemv_fault_flags, kFaultCopyTimeout);
+        return false;
+    };
+    for (Round r = first_round; r.count > 0; r = open_round(r.u + r.count, r.e)) {
+        const Group grp = open_group(r);
+        const int vecs = grp.vecs, slot0 = grp.slot0, my_pair = grp.pair;
+        if (warp == 0 && lane < vecs && my_pair < 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
         if (r.chunk != chunk_of_image) {
-            // every warp has left the previous group's image (the barrier behind its last round)
-            for (int job = warp; job < sbs * p.cap; job += kVWarps) {
-                const int b = job / p.cap, v = job % p.cap;
-                uint8_t* img = image + b * sb_bytes;
-                if (v < vecs) {
-                    const int s = slot0 + v, pair = __ldg(p.g.order + s);
-                    const bool ok = pair >= 0 && pair < p.g.pairs;
-                    const int row = p.g.per_row == 0 ? s : ok ? pair / p.g.per_row : 0;
-                    block_digits(p.x + static_cast<size_t>(row) * p.k + static_cast<size_t>(sb0 + b) * kQK, v, img, meta_offset,
-                                 lane);
-                } else if (v == 1 || v == 3) {
-                    // the other half of a pair of vectors: columns that are never read back, kept finite
-                    *reinterpret_cast<double*>(img + meta_offset + v * kVMetaBytes) = 0.0;
-                }
+            // every warp has left the previous group's image (the barrier behind its last round); a warp's next block
+            // is requested before the digits of the one at hand. The first weights are requested behind the first
+            // digits: beside a full ring of copies everything else that comes from L2, instructions too, waits
+            // microseconds
+            const int jobs = sbs * vecs;
+            float cur[8], nxt[8];
+            if (warp < jobs) fetch(grp, warp, cur);
+            for (int job = warp; job < jobs; job += kVWarps) {
+                if (job + kVWarps < jobs) fetch(grp, job + kVWarps, nxt);
+                const int b = block_of(job, vecs);
+                block_digits(cur, job - b * vecs, image + b * sb_bytes, meta_offset, lane);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cur[e] = nxt[e];
             }
+            if (chunk_of_image < 0)
+                for (int s = 0; s < kVStages; ++s) request();
+            if (vecs & 1)      // the other half of a pair of vectors: never read back, kept finite
+                for (int b = threadIdx.x; b < sbs; b += kVThreads)
+                    *reinterpret_cast<double*>(image + b * sb_bytes + meta_offset + vecs * kVMetaBytes) = 0.0;
             chunk_of_image = r.chunk;
             __syncthreads();
         }
         const int i0 = item_begin(r.count, warp), i1 = item_begin(r.count, warp + 1);
         bool ok = *static_cast<volatile int*>(&sh.abort) == 0;
-        // the group's pairs: vector v's in lane v (-1: not stored)
-        int my_pair = -1;
-        if (lane < vecs) {
-            const int v = __ldg(p.g.order + slot0 + lane);
-            if (v >= 0 && v < p.g.pairs) my_pair = v;
-            else if (warp == 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
-        }
         // y of vector v's pair (v's own lane's, by shuffle) and a row of W
         auto store = [&](int pair, int v, int grow, double a, double b) {
             if (pair < 0 || grow >= p.n) return;
@@ -386,18 +462,17 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         };
         auto run = [&](auto nt_tag) {
             constexpr int NT = decltype(nt_tag)::value;
-            double acc[R][NT][2];
+            // totals of the matrix at hand and of the other one (swapped after every box: one copy of the loop's code)
+            double acc[NT][2], other[NT][2];
             int unit = i0 / boxes, box = i0 - unit * boxes;
             bool whole = true;       // the piece starts at its unit's first box
             for (int it = i0; it < i1 && ok; ++it) {
                 if (it == i0 || box == 0) {
                     whole = box == 0;
 #pragma unroll
-                    for (int m = 0; m < R; ++m)
-#pragma unroll
-                        for (int i = 0; i < NT; ++i) acc[m][i][0] = acc[m][i][1] = 0.0;
+                    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = other[i][0] = other[i][1] = 0.0;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int m = 0; m < R; ++m) {
                     ok = __all_sync(0xFFFFFFFFu,
                                     mbar_try_wait_now(&sh.full[warp][stage], par) ||
@@ -407,40 +482,65 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 #pragma unroll 1
                     for (int b = box * kVBoxCols; b < min(sbs, (box + 1) * kVBoxCols); ++b)
                         superblock_rows<NT>(rows + (b & (kVBoxCols - 1)) * kBlockBytes, image + b * sb_bytes, meta_offset, lane,
-                                            acc[m]);
+                                            acc);
                     __syncwarp();              // every lane has read the box
                     request();
                     if (++stage == kVStages) {
                         stage = 0;
                         par ^= 1u;
                     }
+                    if constexpr (R == 2) {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const double v = acc[i][h];
+                                acc[i][h] = other[i][h];
+                                other[i][h] = v;
+                            }
+                    }
                 }
                 const bool ends = box + 1 == boxes;
-                if (ends || it + 1 == i1) {    // the piece of this unit
+                if (ok && (ends || it + 1 == i1)) {    // the piece of this unit
                     if (!parts_free) {
                         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
                         parts_free = true;
                     }
                     const int t = lane & 3;
-                    double* out = parts + static_cast<size_t>(csize > 1 ? unit + warp : 2 * warp + (whole ? 1 : 0)) * piece;
-                    const int row = (lane >> 2) + 8 * (t & 1);      // even t takes rows 0..7, odd t rows 8..15
+                    // even t holds digits 0 and 1, odd t 2 and 3; even t goes on with row g, odd t with g + 8
+                    const int row = (lane >> 2) + 8 * (t & 1);
+                    const bool head = csize > 1 || !whole;     // goes to shared memory
+                    double* out = parts + static_cast<size_t>(csize > 1 ? unit + warp : warp) * piece + row;
+                    if (csize == 1 && whole && !ends) {        // the rest of the unit: the next warps' heads
+                        for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
+                            if (item_begin(r.count, w) < item_begin(r.count, w + 1)) ok = wait_head(w, round_no) && ok;
+                    }
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
+                        const int vec = 2 * i + (t >> 1);
                         double v[2];
 #pragma unroll
                         for (int m = 0; m < R; ++m) {
-                            const double lo = acc[m][i][0] + __shfl_xor_sync(0xFFFFFFFFu, acc[m][i][0], 1);
-                            const double hi = acc[m][i][1] + __shfl_xor_sync(0xFFFFFFFFu, acc[m][i][1], 1);
-                            v[m] = (t & 1) ? hi : lo;
+                            const double a0 = m == 0 ? acc[i][0] : other[i][0], a1 = m == 0 ? acc[i][1] : other[i][1];
+                            const double mine = (t & 1) ? a1 * 65536.0 : a0, give = (t & 1) ? a0 * 65536.0 : a1;
+                            v[m] = mine + __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+                            if (head) out[(m * p.cap + vec) * kVRows] = v[m];
                         }
-                        const int vec = 2 * i + (t >> 1);
                         const int pair = __shfl_sync(0xFFFFFFFFu, my_pair, vec);
-                        if (csize == 1 && whole && ends) {
-                            store(pair, vec, (r.tile + unit) * kVRows + row, v[0], v[R - 1]);
-                        } else {
+                        if (!head) {
+                            if (!ends)
+                                for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
+                                    if (item_begin(r.count, w) < item_begin(r.count, w + 1)) {
 #pragma unroll
-                            for (int m = 0; m < R; ++m) out[(m * p.cap + vec) * kVRows + row] = v[m];
+                                        for (int m = 0; m < R; ++m)
+                                            v[m] += parts[static_cast<size_t>(w) * piece + (m * p.cap + vec) * kVRows + row];
+                                    }
+                            if (ok) store(pair, vec, (r.tile + unit) * kVRows + row, v[0], v[R - 1]);
                         }
+                    }
+                    if (head && csize == 1) {
+                        __syncwarp();
+                        if (lane == 0) publish_head(round_no);
                     }
                 }
                 if (++box == boxes) {
@@ -452,37 +552,17 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         if (vecs <= 2) run(std::integral_constant<int, 1>{});
         else run(std::integral_constant<int, 2>{});
         if (!ok) sh.abort = 1;
-        if (!parts_free) {       // a warp without items in this round
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-            parts_free = true;
-        }
-        __syncwarp();
-        if (csize > 1) cluster_sync();
-        else __syncthreads();
-        const bool sound = *static_cast<volatile int*>(&sh.abort) == 0;
+        ++round_no;
         if (csize == 1) {
-            // Units cut between warps: warp w adds the unit its range starts inside, if no earlier warp's does: the
-            // tail of the warp before (with items), then the heads of w, w + 1, ...; lane = 16 (vector & 1) + row.
-            const int unit = i0 / boxes;
-            const int prev = i0 > 0 ? static_cast<int>((static_cast<long long>(i0) * kVWarps - 1) / (r.count * boxes)) : 0;
-            if (sound && i0 < i1 && i0 > unit * boxes && item_begin(r.count, prev) <= unit * boxes) {
-                const int row = lane & 15;
-                for (int v = lane >> 4; v - (lane >> 4) < vecs; v += 2) {
-                    double sum[2] = {0.0, 0.0};
-#pragma unroll
-                    for (int m = 0; m < R; ++m) {
-                        const int at = (m * p.cap + v) * kVRows + row;
-                        double d = v < vecs ? parts[(2 * prev + 1) * piece + at] : 0.0;
-                        for (int w = warp; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
-                            if (v < vecs && item_begin(r.count, w) < item_begin(r.count, w + 1)) d += parts[2 * w * piece + at];
-                        sum[m] = d;
-                    }
-                    const int pair = __shfl_sync(0xFFFFFFFFu, my_pair, v & 31);
-                    store(v < vecs ? pair : -1, v, (r.tile + unit) * kVRows + row, sum[0], sum[R - 1]);
-                }
-            }
-            __syncthreads();
+            __syncthreads();         // every warp has left the image and the heads
         } else {
+            if (!parts_free) {       // a warp without items in this round
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                parts_free = true;
+            }
+            __syncwarp();
+            cluster_sync();
+            const bool sound = *static_cast<volatile int*>(&sh.abort) == 0;
             // Totals: thread = (unit, vector, row), the cluster's CTAs take alternate units; pieces in order of CTA and warp.
             const int items = r.count * boxes;
             for (int i = threadIdx.x; i < r.count * p.cap * kVRows; i += kVThreads) {
@@ -587,8 +667,8 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     // average (the image is half as large). The smallest cluster whose CTAs'
     // parts of K fit (groups of two if none does).
     int csize = 1, cap = g.pairs <= g.experts ? 2 : kVMaxVec;
-    while (csize < kVMaxCluster && (nsb + csize - 1) / csize > v_max_sbs(cap, swiglu)) csize *= 2;
-    if ((nsb + csize - 1) / csize > v_max_sbs(cap, swiglu)) cap = 2;
+    while (csize < kVMaxCluster && (nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) csize *= 2;
+    if ((nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) cap = 2;
     const int clusters = gemv_clusters(csize, dev.sm_count);
     if (clusters <= 0) return cuda_failure(cudaErrorInvalidConfiguration);
     MoeGemvParams p{};
@@ -604,7 +684,7 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * csize));
     cfg.blockDim = dim3(kVThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(v_smem(p.part_sbs, cap, swiglu));
+    cfg.dynamicSmemBytes = static_cast<size_t>(v_smem(p.part_sbs, cap, swiglu, csize == 1));
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
