@@ -139,6 +139,19 @@ def library() -> ctypes.CDLL:
     return _lib
 
 
+_torch = None            # torch, imported by the first call that takes a tensor or torch's current stream
+_dtypes: dict = {}       # its element types by name
+
+
+def _import_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _dtypes.update({name: getattr(torch, name) for name in ("float32", "float16", "int32", "uint8")})
+        _torch = torch
+    return _torch
+
+
 def _ptr(t, dtype: str | None = None, name: str = "", min_bytes: int = 0) -> int | None:
     """Device address of a tensor (or a raw integer address, passed through
     unchecked: the caller vouches for it).
@@ -152,17 +165,17 @@ def _ptr(t, dtype: str | None = None, name: str = "", min_bytes: int = 0) -> int
         return None
     if isinstance(t, int):
         return t
-    if dtype is not None and str(t.dtype).replace("torch.", "") != dtype:
+    torch = _torch or _import_torch()
+    if dtype is not None and t.dtype is not _dtypes[dtype]:
         raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name or 'tensor'} must be a CUDA tensor, got device {t.device}")
-    import torch
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name or 'tensor'} is on {t.device}, but the current CUDA device is "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name or 'tensor'} must be contiguous")
-    have = t.numel() * t.element_size()
+    have = t.nbytes
     if have < min_bytes:
         raise ValueError(f"{name or 'tensor'} holds {have} bytes, the call needs {min_bytes}")
     return t.data_ptr()
@@ -180,8 +193,11 @@ def _gemv_sizes_valid(m: int, n: int, k: int) -> bool:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream() builds a Stream object per call; its address is all that is needed
+        torch = _torch or _import_torch()
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

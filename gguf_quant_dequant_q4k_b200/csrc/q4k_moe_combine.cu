@@ -7,6 +7,7 @@
 // 16-byte loads) before it adds the first, so the loads are in flight together.
 #include "q4k_internal.h"
 #include "q4k_moe.h"
+#include "q4k_sm100.cuh"
 
 namespace q4k {
 
@@ -19,6 +20,8 @@ template <int K>
 __global__ void __launch_bounds__(kCombineThreads)
 q4k_moe_combine_kernel(const float* __restrict__ z, const int* __restrict__ ids, const float* __restrict__ weights,
                        const float* residual, float* y, long long n_tokens, int top_k, int cols4) {
+    pdl_launch_dependents();
+    pdl_wait();
     const long long total = n_tokens * cols4;
     const long long stride = static_cast<long long>(gridDim.x) * kCombineThreads;
     const int kk = K > 0 ? K : top_k;
@@ -59,18 +62,22 @@ int launch_moe_combine(const float* z, const int* ids, const float* weights, con
     long long blocks = (total + kCombineThreads - 1) / kCombineThreads;
     const long long cap = static_cast<long long>(num_sms) * 8;
     if (blocks > cap) blocks = cap;
-    const unsigned g = static_cast<unsigned>(blocks);
-#define Q4K_COMBINE(K) \
-    q4k_moe_combine_kernel<K><<<g, kCombineThreads, 0, stream>>>(z, ids, weights, residual, y, n_tokens, top_k, cols4)
-    switch (top_k) {
-        case 1: Q4K_COMBINE(1); break;
-        case 2: Q4K_COMBINE(2); break;
-        case 4: Q4K_COMBINE(4); break;
-        case 8: Q4K_COMBINE(8); break;
-        default: Q4K_COMBINE(0); break;
-    }
-#undef Q4K_COMBINE
-    const cudaError_t e = cudaGetLastError();
+    auto* kernel = top_k == 1   ? q4k_moe_combine_kernel<1>
+                   : top_k == 2 ? q4k_moe_combine_kernel<2>
+                   : top_k == 4 ? q4k_moe_combine_kernel<4>
+                   : top_k == 8 ? q4k_moe_combine_kernel<8>
+                                : q4k_moe_combine_kernel<0>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, z, ids, weights, residual, y, static_cast<long long>(n_tokens),
+                                             top_k, cols4);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 
