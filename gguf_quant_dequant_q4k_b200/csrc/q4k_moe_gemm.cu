@@ -58,41 +58,40 @@ constexpr int kPlainChunk = 4;               // superblocks per accumulation in 
 constexpr int kMaxWStages = 6, kMaxBStages = 6;
 constexpr int kDecodeWarp0 = 4;
 
-// The two shapes of the kernel. Warps: 0 weight copies, 1 activation copies, 2
-// MMA, 3 TMEM; from 4 the decode sets (a warp per lane quarter each); then eight
-// epilogue warps (two per lane quarter).
-// * Wide (large groups): blocks of 256 slots, so that a step's MMAs (1024
-//   cycles) cover the decoding of its weights (650 on two sets) and the issue of
-//   the MMAs (49 cycles each). One accumulator; the epilogue takes it into
-//   registers at once (128 columns per thread) and the MMAs go on.
-// * Narrow (groups of about a hundred or fewer): blocks of 128 slots, where the
-//   decoding sets the pace: three sets (a step's two groups take 626 cycles on 8
-//   warps, 507 on 12, 499 on 16), two accumulators.
-// Both keep four steps of decoded weights in TMEM: with two, the chain MMAs done
-// -> store -> MMAs issued (about 1500 cycles) set the pace (2048 tokens, 14336 x
-// 4096: 1080 cycles per step of 704).
-// Registers move from the copy and decode warps to the epilogue:
-// 640 x 96 = 128 x 48 + 256 x 64 + 256 x 152; 768 x 80 >= 128 x 48 + 384 x 72 +
-// 256 x 104.
-template <bool WIDE>
+// The shapes of the kernel. Warps: 0 weight copies, 1 activation copies, 2 MMA, 3
+// TMEM; 4-15 decode (three sets of a warp per lane quarter: a step's two groups
+// take 626 cycles on 8 warps alone, 507 on 12, 499 on 16); 16-23 epilogue (two
+// per lane quarter).
+// * Wide (large groups): blocks of 256 slots (plain: 192), so that a step's MMAs
+//   (4 cycles per slot) cover the decoding of its weights and the issue of the
+//   MMAs. One accumulator, taken into registers by the epilogue, 64 columns per
+//   thread at a time (SwiGLU), or added to the registers' sums (plain).
+// * Narrow (groups of about a hundred or fewer): blocks of 128 slots, two
+//   accumulators; the decoding sets the pace.
+// All keep at least four steps of decoded weights in TMEM: with two, the chain
+// MMAs done -> store -> MMAs issued (about 1500 cycles) set the pace (2048
+// tokens, 14336 x 4096: 1080 cycles per step of 704).
+// Registers move from the copy and decode warps to the epilogue: 768 x 80 = 128 x
+// 48 + 384 x 64 + 256 x 120 (plain, wide) >= 128 x 48 + 384 x 72 + 256 x 104.
+template <bool SWIGLU, bool WIDE>
 struct MoeShape {
-    static constexpr int slots = WIDE ? 256 : 128;           // most slots per tile: MMA N
+    static constexpr int slots = !WIDE ? 128 : SWIGLU ? 256 : 192;   // most slots per tile: MMA N
     static constexpr int d_bufs = WIDE ? 1 : 2;
     static constexpr int a_col0 = slots * d_bufs;            // TMEM: D, then A
     static constexpr int a_bufs = (kMoeTmemCols - a_col0) / (kGroup / 2);   // decoded groups
-    static constexpr int sets = WIDE ? 2 : 3;
+    static constexpr int sets = 3;
     static constexpr int epi_warp0 = kDecodeWarp0 + 4 * sets;
     static constexpr int threads = 32 * (epi_warp0 + 8);
-    static constexpr int regs_launch = WIDE ? 96 : 80, regs_copy = 48, regs_decode = WIDE ? 64 : 72,
-                         regs_epi = WIDE ? 152 : 104;
-    static constexpr int b_stages = WIDE ? 4 : 6, w_stages = WIDE ? 4 : 6;
+    static constexpr int regs_launch = 80, regs_copy = 48, regs_decode = WIDE && !SWIGLU ? 64 : 72,
+                         regs_epi = WIDE && !SWIGLU ? 120 : 104;
+    static constexpr int b_stages = !WIDE ? 6 : SWIGLU ? 4 : 5, w_stages = WIDE ? 4 : 6;
     static constexpr int b_half = slots / 2 * kGroup * 2;    // 64 elements of the CTA's rows of B
     static constexpr int b_stage = 2 * b_half;
     static constexpr int smem = 1024 + b_stages * b_stage + w_stages * kWStageBytes;
     static_assert(threads * regs_launch <= 65536 &&
                       128 * regs_copy + 128 * sets * regs_decode + 256 * regs_epi <= threads * regs_launch,
                   "register split");
-    static_assert(b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
+    static_assert(a_bufs % 2 == 0 && b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");
 };
 constexpr int kNarrowPairsPerExpert = 96;    // at most this many pairs per expert on average: narrow
@@ -222,10 +221,10 @@ __device__ __forceinline__ void decode_group(const QuantGroup& in, uint32_t (&ou
 }
 
 template <bool SWIGLU, bool WIDE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MoeShape<WIDE>::threads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MoeShape<SWIGLU, WIDE>::threads, 1)
 q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_w2,
                     const __grid_constant__ CUtensorMap map_x, const MoeGemmParams p) {
-    using S = MoeShape<WIDE>;
+    using S = MoeShape<SWIGLU, WIDE>;
     constexpr int kBStages = S::b_stages, kWStages = S::w_stages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -493,54 +492,77 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     else if (t.row_tile == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
                 }
             }
-            float acc[kPart];
-            for (int b = 0; b < nsb; b += SWIGLU ? nsb : kPlainChunk) {
+            if constexpr (SWIGLU) {
                 const int dbuf = chunk_no % S::d_bufs;
                 ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / S::d_bufs) & 1));
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
                 ++chunk_no;
                 tc_fence_after_sync();
-                // D into registers; from the second chunk on, added to them
-#pragma unroll
-                for (int j = 0; j < kPart / 8; ++j) {
-                    if (c0 + 8 * j < t.cols) {
-                        uint32_t r[8];
-                        tmem_load_8cols(lane_addr + dbuf * S::slots + 8 * j, r);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            acc[8 * j + c] = SWIGLU || b == 0 ? __uint_as_float(r[c]) : acc[8 * j + c] + __uint_as_float(r[c]);
-                    }
-                }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
-            }
-            if (!ok) {
-                *abort_flag = 1;
-                break;
-            }
-            if constexpr (SWIGLU) {
                 const int feature = (t.row_tile * 2 + static_cast<int>(rank)) * 64 + 16 * quarter + (lane & 15);
                 const bool gate = lane < 16;
                 // lanes with gate rows finish even columns, lanes with up rows odd ones
                 __half* y = static_cast<__half*>(p.y) + static_cast<size_t>(t.slot0 + c0 + (gate ? 0 : 1)) * p.n + feature;
 #pragma unroll
-                for (int j = 0; j < kPart / 32; ++j) {
-                    const uint32_t stored = __ballot_sync(0xFFFFFFFFu, pair[j] >= 0);
-                    const uint32_t mine = feature < p.n ? stored >> (gate ? 0 : 1) : 0u;
-                    if (stored == 0u) continue;
+                for (int pass = 0; pass < kPart / 64; ++pass) {
+                    uint32_t acc[2][32];
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float a = acc[32 * j + c], d = acc[32 * j + c + 1];
-                        const float other = __shfl_xor_sync(0xFFFFFFFFu, gate ? d : a, 16);
-                        if (mine & (1u << c))
-                            y[static_cast<size_t>(32 * j + c) * p.n] =
-                                __float2half_rn(silu_mul_fast(gate ? a : other, gate ? other : d));
+                    for (int j = 0; j < 2; ++j)
+                        if (c0 + 64 * pass + 32 * j < t.cols)
+                            tmem_load_32cols_async(lane_addr + dbuf * S::slots + 64 * pass + 32 * j, acc[j]);
+                    tmem_wait_ld();
+                    if (pass + 1 == kPart / 64) {       // D is in registers: the MMAs may go on
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t stored = __ballot_sync(0xFFFFFFFFu, pair[2 * pass + j] >= 0);
+                        const uint32_t mine = feature < p.n ? stored >> (gate ? 0 : 1) : 0u;
+                        if (stored == 0u) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float a = __uint_as_float(acc[j][c]), d = __uint_as_float(acc[j][c + 1]);
+                            const float other = __shfl_xor_sync(0xFFFFFFFFu, gate ? d : a, 16);
+                            if (mine & (1u << c))
+                                y[static_cast<size_t>(64 * pass + 32 * j + c) * p.n] =
+                                    __float2half_rn(silu_mul_fast(gate ? a : other, gate ? other : d));
+                        }
                     }
                 }
             } else {
+                float acc[kPart];
+                for (int b = 0; b < nsb; b += kPlainChunk) {
+                    const int dbuf = chunk_no % S::d_bufs;
+                    ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / S::d_bufs) & 1));
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    ++chunk_no;
+                    tc_fence_after_sync();
+                    // D into registers; from the second chunk on, added to them
+#pragma unroll
+                    for (int j = 0; j < kPart / 8; ++j) {
+                        if (c0 + 8 * j < t.cols) {
+                            uint32_t r[8];
+                            tmem_load_8cols(lane_addr + dbuf * S::slots + 8 * j, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                acc[8 * j + c] = b == 0 ? __uint_as_float(r[c]) : acc[8 * j + c] + __uint_as_float(r[c]);
+                        }
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&sh.d_empty[dbuf], 0));
+                }
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
                 const int row = (t.row_tile * 2 + static_cast<int>(rank)) * kCtaRows + 32 * quarter + lane;
                 float* y = static_cast<float*>(p.y) + row;
 #pragma unroll
@@ -700,8 +722,9 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
         p.row_tiles = (n + tile_rows - 1) / tile_rows;
         const bool wide = g.pairs > static_cast<long long>(kNarrowPairsPerExpert) * g.experts;
         cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
-        cfg.blockDim = dim3(wide ? MoeShape<true>::threads : MoeShape<false>::threads);
-        cfg.dynamicSmemBytes = wide ? MoeShape<true>::smem : MoeShape<false>::smem;
+        cfg.blockDim = dim3(MoeShape<true, true>::threads);
+        cfg.dynamicSmemBytes = swiglu ? (wide ? MoeShape<true, true>::smem : MoeShape<true, false>::smem)
+                                      : (wide ? MoeShape<false, true>::smem : MoeShape<false, false>::smem);
         auto* kernel = swiglu ? (wide ? q4k_moe_gemm_kernel<true, true> : q4k_moe_gemm_kernel<true, false>)
                               : (wide ? q4k_moe_gemm_kernel<false, true> : q4k_moe_gemm_kernel<false, false>);
         e = cudaLaunchKernelEx(&cfg, kernel, mw, mw2, mx, p);
@@ -715,10 +738,10 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
 
 int moe_gemm_set_attributes() {
     constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, true>, attr, MoeShape<true>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, false>, attr, MoeShape<false>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, true>, attr, MoeShape<true>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, false>, attr, MoeShape<false>::smem);
+    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, true>, attr, MoeShape<true, true>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, false>, attr, MoeShape<true, false>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, true>, attr, MoeShape<false, true>::smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, false>, attr, MoeShape<false, false>::smem);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 
