@@ -414,7 +414,7 @@ int check_moe_product(const void* w, const void* w2, bool swiglu, const void* x,
          overlaps(y, ybytes, offsets, static_cast<size_t>(n_experts + 1) * 4) ||
          overlaps(y, ybytes, order, static_cast<size_t>(n_pairs) * 4)))
         return Q4K_ERR_OVERLAP;
-    *g = MoeGroups{offsets, order, n_experts, n_pairs, per_row, x_rows};
+    *g = MoeGroups{offsets, order, n_experts, n_pairs, per_row};
     return Q4K_OK;
 }
 

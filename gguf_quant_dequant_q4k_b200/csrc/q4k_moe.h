@@ -17,7 +17,6 @@ struct MoeGroups {
     int experts;
     int pairs;
     int per_row;          // x row of slot s: s if 0, else order[s] / per_row
-    int x_rows;           // rows of x
 };
 
 int launch_moe_route(const float* logits, int* ids, float* weights, int* offsets, int* order, int n_tokens,

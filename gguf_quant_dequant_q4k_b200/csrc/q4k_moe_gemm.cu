@@ -536,6 +536,8 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 }
             } else {
                 float acc[kPart];
+#pragma unroll
+                for (int c = 0; c < kPart; ++c) acc[c] = 0.f;
                 for (int b = 0; b < nsb; b += kPlainChunk) {
                     const int dbuf = chunk_no % S::d_bufs;
                     ok = !*abort_flag && moe_wait(&sh.d_full[dbuf], static_cast<uint32_t>((chunk_no / S::d_bufs) & 1));
@@ -543,16 +545,14 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (!ok) break;
                     ++chunk_no;
                     tc_fence_after_sync();
-                    // D into registers; from the second chunk on, added to them
 #pragma unroll
-                    for (int j = 0; j < kPart / 8; ++j) {
-                        if (c0 + 8 * j < t.cols) {
-                            uint32_t r[8];
-                            tmem_load_8cols(lane_addr + dbuf * S::slots + 8 * j, r);
+                    for (int j = 0; j < kPart / 16; ++j) {
+                        if (c0 + 16 * j < t.cols) {
+                            uint32_t r[16];
+                            tmem_load_16cols(lane_addr + dbuf * S::slots + 16 * j, r);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                acc[8 * j + c] = b == 0 ? __uint_as_float(r[c]) : acc[8 * j + c] + __uint_as_float(r[c]);
+                            for (int c = 0; c < 16; ++c) acc[16 * j + c] += __uint_as_float(r[c]);
                         }
                     }
                     tc_fence_before_sync();
@@ -588,23 +588,33 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     }
 }
 
-// out[s] = x[order[s] / per_row], s < offsets[experts], 16 bytes per thread and
-// step. A bad entry takes row 0 (the product does not store its slot).
+// out[s] = x[order[s] / per_row], s < offsets[experts]: a warp per row, four
+// 16-byte loads per lane in flight. A bad entry takes row 0 (the product does
+// not store its slot).
 constexpr int kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads)
 q4k_moe_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, const MoeGroups g, int row16) {
     pdl_launch_dependents();
     pdl_wait();
+    const int lane = threadIdx.x & 31;
     const int slots = min(g.pairs, __ldg(g.offsets + g.experts));
-    const long long total = static_cast<long long>(slots) * row16;
-    const long long stride = static_cast<long long>(gridDim.x) * kGatherThreads;
-    for (long long i = static_cast<long long>(blockIdx.x) * kGatherThreads + threadIdx.x; i < total; i += stride) {
-        const long long s = i / row16;
-        const int c = static_cast<int>(i - s * row16);
+    const int warps = static_cast<int>(gridDim.x) * (kGatherThreads / 32);
+    for (int s = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5); s < slots;
+         s += warps) {
         const int pair = __ldg(g.order + s);
         const int row = pair >= 0 && pair < g.pairs ? pair / g.per_row : 0;
-        out[i] = __ldg(x + static_cast<long long>(row) * row16 + c);
+        const uint4* src = x + static_cast<size_t>(row) * row16;
+        uint4* dst = out + static_cast<size_t>(s) * row16;
+        for (int c0 = lane; c0 < row16; c0 += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c0 + 32 * i < row16) v[i] = __ldg(src + c0 + 32 * i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (c0 + 32 * i < row16) dst[c0 + 32 * i] = v[i];
+        }
     }
 }
 
@@ -649,9 +659,13 @@ bool make_moe_x_map(CUtensorMap* map, const void* x, int rows, int k, int box_ro
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The current device's pool for the copies of x: it keeps its memory between
-// calls (the default pool gives it back whenever the device is synchronised,
-// and the next allocation then takes 0.5-1.6 ms).
+// The current device's pool for the copies of x: it keeps up to kPoolKeepBytes
+// between calls (the default pool gives all back whenever the device is
+// synchronised, and the next allocation then takes 0.5-1.6 ms). Allocations and
+// frees are stream-ordered and captured into graphs as their own nodes, so no
+// two calls that may overlap share a copy.
+constexpr uint64_t kPoolKeepBytes = 512ull << 20;
+
 cudaError_t workspace_pool(cudaMemPool_t* pool) {
     constexpr int kDevices = 64;
     static std::once_flag once[kDevices];
@@ -662,14 +676,20 @@ cudaError_t workspace_pool(cudaMemPool_t* pool) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
+        // the first call may be inside a capture, which a pool's creation would end in the default mode
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        status[dev] = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (status[dev] != cudaSuccess) return;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         status[dev] = cudaMemPoolCreate(&pools[dev], &props);
-        uint64_t keep = UINT64_MAX;
+        uint64_t keep = kPoolKeepBytes;
         if (status[dev] == cudaSuccess)
             status[dev] = cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &keep);
+        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (status[dev] == cudaSuccess) status[dev] = back;
     });
     *pool = pools[dev];
     return status[dev];
@@ -700,7 +720,8 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
         if (e == cudaSuccess)
             e = cudaMallocFromPoolAsync(&work, static_cast<size_t>(g.pairs) * static_cast<size_t>(k) * 2, pool, stream);
         if (e != cudaSuccess) return cuda_failure(e);
-        const long long blocks = (static_cast<long long>(g.pairs) * (k / 8) + kGatherThreads - 1) / kGatherThreads;
+        const int per_cta = kGatherThreads / 32;
+        const long long blocks = (static_cast<long long>(g.pairs) + per_cta - 1) / per_cta;
         cfg.gridDim = dim3(static_cast<unsigned>(blocks < dev.sm_count * 8 ? blocks : dev.sm_count * 8));
         cfg.blockDim = dim3(kGatherThreads);
         e = cudaLaunchKernelEx(&cfg, q4k_moe_gather_kernel, static_cast<const uint4*>(x_f16), static_cast<uint4*>(work), g,

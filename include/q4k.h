@@ -520,7 +520,13 @@ Q4K_API int q4k_moe_gemv_swiglu(const void *w_gate, const void *w_up, const floa
  * memory (W16_e: the values q4k_dequant_f16 gives, formed inside the kernel).
  *   x_f16: binary16 rows (q4k_f32_to_f16); y: float32, 4-byte aligned, rows in
  *   pair order.
- * Accuracy: as q4k_gemm_f16. Returns a q4k_status.
+ * Accuracy: as q4k_gemm_f16 with K at most 1024 (longer sums are carried in f32
+ * registers, rounded to nearest).
+ * Workspace (this and the SwiGLU form): with pairs_per_row > 0 the rows of x are
+ * first copied into slot order, n_pairs * K * 2 bytes allocated and freed
+ * stream-ordered from a memory pool of the library's own (capturable in a CUDA
+ * graph; the pool keeps up to 512 MiB for later calls). pairs_per_row == 0
+ * allocates nothing. Returns a q4k_status.
  */
 Q4K_API int q4k_moe_gemm_f16(const void *w, const void *x_f16, const int *offsets, const int *order,
                              float *y, int n_experts, int n_pairs, int pairs_per_row, int n, int k,
@@ -529,7 +535,8 @@ Q4K_API int q4k_moe_gemm_f16(const void *w, const void *x_f16, const int *offset
 /*
  * h16[s] = binary16 of silu(g) * u, g = x16[row(s)] * Wg16_e^T and
  * u = x16[row(s)] * Wu16_e^T, rows in slot order, 16-byte aligned: the x_f16
- * of the down projection (pairs_per_row 0).
+ * of the down projection (pairs_per_row 0). g and u carry the q4k_gemm_f16
+ * bound; the epilogue's f32 error is far below the one rounding to binary16.
  * Returns a q4k_status.
  */
 Q4K_API int q4k_moe_gemm_swiglu_f16(const void *w_gate, const void *w_up, const void *x_f16,

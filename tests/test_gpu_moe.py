@@ -211,7 +211,7 @@ GEMM_CASES = [
     (1, 1, 1, 1, 256, 0), (1, 4, 2, 3, 512, 0), (3, 3, 1, 15, 768, 0), (17, 2, 2, 63, 512, 1), (40, 8, 2, 64, 1024, 3),
     (100, 4, 3, 65, 256, 0), (129, 1, 1, 128, 512, 0), (300, 3, 2, 130, 768, 7), (257, 2, 1, 200, 1280, 0),
     (600, 4, 2, 257, 512, 11), (64, 40, 6, 100, 1024, 1), (260, 2, 2, 96, 4096, 0), (150, 2, 1, 70, 14336, 0),
-    (1100, 2, 1, 129, 256, 0),
+    (1100, 2, 1, 129, 256, 0), (257, 1, 1, 300, 512, 0), (192, 1, 1, 260, 2304, 0), (193, 1, 1, 130, 1280, 1),
 ]
 
 
@@ -379,6 +379,38 @@ def test_graph_capture_and_two_streams(q4k, half, mats):
     torch.cuda.synchronize()
     for got, wanted in outs:
         assert torch.equal(got, wanted)
+
+
+FIRST_CALL_IN_CAPTURE = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import gguf_quant_dequant_q4k_b200 as q4k
+import test_gpu_moe as t
+p = t.Problem(20, 4, 2, 200, 1024, 18, mats=2, half=True)
+d = t.Problem(20, 4, 2, 96, 1024, 19, mats=1, half=False)
+y, z = p.out(torch.float16), d.out(torch.float32)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    t.run_product(q4k, p, y)
+    t.run_product(q4k, d, z)
+g.replay()
+g.replay()
+t.check_product(p, y, "captured first call")
+t.check_product(d, z, "captured first call")
+print("captured ok")
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    """Nothing the first call sets up (attributes, the workspace pool) breaks a capture."""
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    out = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_CAPTURE % (os.path.dirname(here), here)], timeout=300,
+                         capture_output=True, text=True)
+    assert out.returncode == 0 and "captured ok" in out.stdout, out.stderr[-2000:]
 
 
 @pytest.mark.parametrize("half", [False, True])
