@@ -54,7 +54,7 @@ constexpr int kGroup = 64;                   // weights of one quant group of a 
 constexpr int kStep = 2 * kGroup;            // K per step
 constexpr int kBBoxRows = 32;                // rows per TMA box of x
 constexpr int kMoeTmemCols = 512;
-constexpr int kPlainChunk = 4;               // superblocks per accumulation in D, plain form
+constexpr int kPlainChunk = 3;               // superblocks per accumulation in D, plain form
 constexpr int kMaxWStages = 6, kMaxBStages = 6;
 constexpr int kDecodeWarp0 = 4;
 

@@ -520,7 +520,7 @@ Q4K_API int q4k_moe_gemv_swiglu(const void *w_gate, const void *w_up, const floa
  * memory (W16_e: the values q4k_dequant_f16 gives, formed inside the kernel).
  *   x_f16: binary16 rows (q4k_f32_to_f16); y: float32, 4-byte aligned, rows in
  *   pair order.
- * Accuracy: as q4k_gemm_f16 with K at most 1024 (longer sums are carried in f32
+ * Accuracy: as q4k_gemm_f16 with K at most 768 (longer sums are carried in f32
  * registers, rounded to nearest).
  * Workspace (this and the SwiGLU form): with pairs_per_row > 0 the rows of x are
  * first copied into slot order, n_pairs * K * 2 bytes allocated and freed
