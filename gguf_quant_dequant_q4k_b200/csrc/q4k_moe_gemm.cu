@@ -4,19 +4,20 @@
 // binary16), formed inside the kernel from the superblocks.
 //
 // * Tiles. A pair of CTAs (one cluster, tensor cores joined by cta_group::2)
-//   owns a tile of y^T: 256 rows of W_e (the MMA's M, 128 per CTA) by up to 192
-//   slots of expert e (N). An expert's slots are cut into equal blocks of at
-//   most 192; N is the block's slots rounded up to 16. SwiGLU: 128 gate and 128
-//   up rows, per CTA 64 and 64, so that TMEM lanes 32q + l and 32q + 16 + l
-//   (l < 16) hold gate and up of one feature. 74 persistent pairs walk the
+//   owns a tile of y^T: 256 rows of W_e (the MMA's M, 128 per CTA) by a block of
+//   expert e's slots (N). An expert's slots are cut into equal blocks of at most
+//   MoeShape::slots; N is the block's slots rounded up to 16. SwiGLU: 128 gate
+//   and 128 up rows, per CTA 64 and 64, so that TMEM lanes 32q + l and 32q + 16 +
+//   l (l < 16) hold gate and up of one feature. 74 persistent pairs walk the
 //   tiles of all experts, the blocks of a row tile one after another.
 // * A (weights). A producer streams 128 rows x 144 bytes per superblock into a
 //   shared-memory ring (TMA). Three sets of four decode warps (a warp per TMEM
 //   lane quarter, a lane per row) take the 64-weight quant groups in turn: the
 //   quants become f32 through binary16 subnormals, the weight is one packed fma,
 //   rounded once, then cvt to fp16 pairs, stored to TMEM. The decoded group
-//   feeds all N slots, so the decoding hides behind the MMAs (8 N cycles per
-//   superblock) where N is large enough.
+//   feeds all N slots: a step's MMAs take 4 N cycles, its decoding about 950
+//   (408 issue slots on each SM sub-partition without any wait), so blocks of
+//   about 230 slots and more hide it.
 // * B (activations). 128 elements of N / 2 rows per CTA and step, by TMA in the
 //   128-byte-swizzled layout; the pair's tensor cores share the two halves. x
 //   in slot order is read in place; otherwise a copy in slot order is made
@@ -24,11 +25,17 @@
 //   2048 tokens, top 2, 14336x4096: fetching each row inside the kernel with
 //   16-byte async copies took 54 cycles per 512 bytes (1.23 ms in all), with
 //   four-row TMA gathers about 90 cycles (2.8 ms).
-// * D. Two TMEM accumulators of 192 columns take turns: the epilogue empties
-//   one while the MMAs fill the other. The tensor core adds to D by truncation
-//   (measured 1.7e-5 relative over K = 14336); every kPlainChunk superblocks
-//   the plain form therefore moves D into f32 registers, rounding to nearest
-//   (under 1e-6). The SwiGLU form rounds to fp16 and keeps D for the whole row.
+// * D. The tensor core adds to D by truncation (measured 1.7e-5 relative over K =
+//   14336); every kPlainChunk superblocks the plain form therefore moves D into
+//   f32 registers, rounding to nearest (under 1e-6). The SwiGLU form rounds to
+//   fp16 and keeps D for the whole row.
+// * Measured (times are of calls back to back; the clock falls to about 1.5 GHz
+//   under the large cases): 2048 tokens, 8 experts, top 2: gate/up 14336 x 4096
+//   0.82-0.93 ms = 1030-1170 TFLOP/s (cuBLAS bf16, sustained: 1428), bound by
+//   the MMAs, 1126 cycles per step of about 910; down 4096 x 14336 0.49-0.56 ms,
+//   bound by the decoding and the drains of D. 777 tokens, 64 experts, top 4
+//   (about 48 slots each): gate/up 1536 x 2048 112-128 us, down 62-67 us, bound
+//   by the decoding (975 cycles per step).
 // * Waits are bounded; a role that gives up raises Q4K_FAULT_COPY_TIMEOUT and
 //   the CTA lets its copies and MMAs land before shared memory and TMEM go.
 #include <cstdint>
@@ -94,7 +101,10 @@ struct MoeShape {
     static_assert(a_bufs % 2 == 0 && b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");
 };
-constexpr int kNarrowPairsPerExpert = 96;    // at most this many pairs per expert on average: narrow
+// At most this many pairs per expert on average: narrow. (Measured at 512 pairs per
+// expert: wide 743 us against narrow 1000, gate/up; with about 48 the blocks are the
+// same, and narrow keeps two accumulators and six stages.)
+constexpr int kNarrowPairsPerExpert = 96;
 
 struct MoeShared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
