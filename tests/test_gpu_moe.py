@@ -64,7 +64,7 @@ def check_route(got, logits, top_k, renorm, what=""):
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("t,e,top_k", [(1, 1, 1), (1, 8, 2), (3, 2, 2), (7, 31, 3), (24, 64, 8), (33, 32, 16),
                                        (65, 33, 1), (130, 65, 5), (200, 128, 8), (257, 129, 4), (64, 256, 16),
-                                       (1000, 16, 2), (2049, 100, 6), (5000, 255, 8)])
+                                       (1000, 16, 2), (2049, 100, 6), (5000, 255, 8), (50000, 16, 2)])
 def test_route(q4k, t, e, top_k, renorm):
     rng = np.random.default_rng(t * 1000 + e)
     logits = rng.standard_normal((t, e)).astype(np.float32)
@@ -188,7 +188,7 @@ GEMV_CASES = [  # tokens, experts, top_k, n, k, pad
     (1, 8, 8, 130, 1536, 0), (9, 4, 2, 257, 2304, 2), (24, 16, 4, 96, 1280, 3), (33, 2, 2, 64, 512, 0),
     (70, 3, 1, 40, 256, 5), (1, 8, 2, 1000, 4096, 0), (4, 8, 2, 300, 14336, 0), (2, 2, 1, 70, 20736, 0),
     (16, 40, 6, 200, 1024, 1), (5, 2, 1, 17, 28672, 0), (4, 2, 1, 16, 43008, 0), (30, 3, 1, 1030, 2048, 0),
-    (1, 3, 1, 5, 1024, 0), (2, 6, 2, 2400, 1280, 0), (9, 2, 1, 5000, 512, 0), (3, 2, 2, 777, 4096, 0),
+    (1, 3, 1, 5, 1024, 0), (2, 6, 2, 2400, 1280, 0), (500, 4, 3, 40, 256, 9), (10, 256, 16, 20, 256, 1), (9, 2, 1, 5000, 512, 0), (3, 2, 2, 777, 4096, 0),
 ]
 
 
@@ -211,7 +211,7 @@ GEMM_CASES = [
     (1, 1, 1, 1, 256, 0), (1, 4, 2, 3, 512, 0), (3, 3, 1, 15, 768, 0), (17, 2, 2, 63, 512, 1), (40, 8, 2, 64, 1024, 3),
     (100, 4, 3, 65, 256, 0), (129, 1, 1, 128, 512, 0), (300, 3, 2, 130, 768, 7), (257, 2, 1, 200, 1280, 0),
     (600, 4, 2, 257, 512, 11), (64, 40, 6, 100, 1024, 1), (260, 2, 2, 96, 4096, 0), (150, 2, 1, 70, 14336, 0),
-    (1100, 2, 1, 129, 256, 0), (257, 1, 1, 300, 512, 0), (192, 1, 1, 260, 2304, 0), (193, 1, 1, 130, 1280, 1),
+    (1100, 2, 1, 129, 256, 0), (257, 1, 1, 300, 512, 0), (70, 256, 8, 30, 256, 3), (192, 1, 1, 260, 2304, 0), (193, 1, 1, 130, 1280, 1),
 ]
 
 
@@ -220,6 +220,47 @@ GEMM_CASES = [
 def test_gemm_matches_oracle(q4k, tokens, experts, top_k, n, k, pad, mats):
     p = Problem(tokens, experts, top_k, n, k, 90 + tokens + n, pad, mats=mats, half=True)
     check_product(p, run_product(q4k, p), f"{tokens} tokens {experts}x{n}x{k}")
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+def test_gemv_long_rows_in_slot_order(q4k, mats):
+    """Rows of x by slot where K is shared by the CTAs of a cluster."""
+    p = Problem(9, 3, 2, 50, 14336, 79, pad=1, mats=mats, per_row=0)
+    check_product(p, run_product(q4k, p), "long rows")
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("k", [512, 14336])
+def test_nobody_routed(q4k, k, mats, half):
+    """Every pair without an expert: nothing is written, nothing faults."""
+    p = Problem(6, 3, 2, 20, k, 80, mats=mats, half=half, ids=np.full((6, 2), -1, np.int32))
+    y = run_product(q4k, p)
+    torch.cuda.synchronize()
+    assert (y == FILL).all()
+    assert q4k.q4k_device_fault_flags() == 0
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("mats", [1, 2])
+def test_nonfinite_weights_stay_in_their_row(q4k, mats, half):
+    """A row of W whose d is NaN, and one whose dmin is inf: that output feature
+    of that expert's pairs is not finite, everything else keeps its bits."""
+    p = Problem(40, 3, 1, 70, 768, 81, mats=mats, half=half)
+    clean = run_product(q4k, p).float().cpu().numpy()
+    w = p.ws[-1].copy()
+    blocks = w.reshape(3, 70, 3, 144)
+    blocks[1, 17, 2, 0:2] = (0x00, 0x7E)      # d = NaN
+    blocks[1, 33, 0, 2:4] = (0x00, 0x7C)      # dmin = inf
+    blocks[1, 33, 0, 8:12] = 0x3F             # its first mins are not 0
+    p.dw[-1] = dev(w)
+    y = run_product(q4k, p).float().cpu().numpy()
+    slots = slice(int(p.offsets[1]), int(p.offsets[2]))
+    rows = np.arange(p.pairs)[slots] if mats == 2 else p.order[slots]
+    assert rows.size and not np.isfinite(y[np.ix_(rows, [17, 33])]).any()
+    keep = np.ones(y.shape, bool)
+    keep[np.ix_(rows, [17, 33])] = False
+    assert np.array_equal(y[keep], clean[keep])
 
 
 @pytest.mark.parametrize("mats", [1, 2])
