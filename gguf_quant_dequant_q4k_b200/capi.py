@@ -166,6 +166,10 @@ def _ptr(t, dtype: str | None = None, name: str = "", min_bytes: int = 0) -> int
     if isinstance(t, int):
         return t
     torch = _torch or _import_torch()
+    if ((dtype is None or t.dtype is _dtypes[dtype]) and (device := t.get_device()) >= 0
+            and device == torch._C._cuda_getDevice() and t.is_contiguous() and (min_bytes == 0 or t.nbytes >= min_bytes)):
+        return t.data_ptr()
+    # refused: say why
     if dtype is not None and t.dtype is not _dtypes[dtype]:
         raise TypeError(f"{name} must be a {dtype} tensor, got {t.dtype}")
     if not t.is_cuda:
@@ -175,10 +179,7 @@ def _ptr(t, dtype: str | None = None, name: str = "", min_bytes: int = 0) -> int
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name or 'tensor'} must be contiguous")
-    have = t.nbytes
-    if have < min_bytes:
-        raise ValueError(f"{name or 'tensor'} holds {have} bytes, the call needs {min_bytes}")
-    return t.data_ptr()
+    raise ValueError(f"{name or 'tensor'} holds {t.nbytes} bytes, the call needs {min_bytes}")
 
 
 def _need(count: int, item: int, valid: bool) -> int:

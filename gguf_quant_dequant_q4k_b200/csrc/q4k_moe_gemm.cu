@@ -62,7 +62,7 @@ constexpr int kStep = 2 * kGroup;            // K per step
 constexpr int kBBoxRows = 32;                // rows per TMA box of x
 constexpr int kMoeTmemCols = 512;
 constexpr int kPlainChunk = 3;               // superblocks per accumulation in D, plain form
-constexpr int kMaxWStages = 6, kMaxBStages = 6;
+constexpr int kMaxWStages = 4, kMaxBStages = 8;
 constexpr int kDecodeWarp0 = 4;
 
 // The shapes of the kernel. Warps: 0 weight copies, 1 activation copies, 2 MMA, 3
@@ -75,7 +75,7 @@ constexpr int kDecodeWarp0 = 4;
 //   thread at a time (SwiGLU), or added to the registers' sums (plain).
 // * Narrow (groups of about a hundred or fewer): blocks of 128 slots, two
 //   accumulators; the decoding sets the pace.
-// All keep at least four steps of decoded weights in TMEM: with two, the chain
+// All keep four steps of decoded weights in TMEM: with two, the chain
 // MMAs done -> store -> MMAs issued (about 1500 cycles) set the pace (2048
 // tokens, 14336 x 4096: 1080 cycles per step of 704).
 // Registers move from the copy and decode warps to the epilogue: 768 x 80 = 128 x
@@ -85,25 +85,26 @@ struct MoeShape {
     static constexpr int slots = !WIDE ? 128 : SWIGLU ? 256 : 192;   // most slots per tile: MMA N
     static constexpr int d_bufs = WIDE ? 1 : 2;
     static constexpr int a_col0 = slots * d_bufs;            // TMEM: D, then A
-    static constexpr int a_bufs = (kMoeTmemCols - a_col0) / (kGroup / 2);   // decoded groups
+    static constexpr int a_bufs = 8;                         // decoded groups: four steps
     static constexpr int sets = 3;
     static constexpr int epi_warp0 = kDecodeWarp0 + 4 * sets;
     static constexpr int threads = 32 * (epi_warp0 + 8);
     static constexpr int regs_launch = 80, regs_copy = 48, regs_decode = WIDE && !SWIGLU ? 64 : 72,
                          regs_epi = WIDE && !SWIGLU ? 120 : 104;
-    static constexpr int b_stages = !WIDE ? 6 : SWIGLU ? 4 : 5, w_stages = WIDE ? 4 : 6;
+    static constexpr int b_stages = WIDE ? 4 : 8, w_stages = 4;   // powers of two: the decode warps index by masks
     static constexpr int b_half = slots / 2 * kGroup * 2;    // 64 elements of the CTA's rows of B
     static constexpr int b_stage = 2 * b_half;
     static constexpr int smem = 1024 + b_stages * b_stage + w_stages * kWStageBytes;
     static_assert(threads * regs_launch <= 65536 &&
                       128 * regs_copy + 128 * sets * regs_decode + 256 * regs_epi <= threads * regs_launch,
                   "register split");
-    static_assert(a_bufs % 2 == 0 && b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
+    static_assert(a_col0 + a_bufs * kGroup / 2 <= kMoeTmemCols, "TMEM");
+    static_assert(b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");
 };
 // At most this many pairs per expert on average: narrow. (Measured at 512 pairs per
 // expert: wide 743 us against narrow 1000, gate/up; with about 48 the blocks are the
-// same, and narrow keeps two accumulators and six stages.)
+// same, and narrow keeps two accumulators and eight stages.)
 constexpr int kNarrowPairsPerExpert = 96;
 
 struct MoeShared {
@@ -535,12 +536,16 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         const uint32_t mine = feature < p.n ? stored >> (gate ? 0 : 1) : 0u;
                         if (stored == 0u) continue;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float a = __uint_as_float(acc[j][c]), d = __uint_as_float(acc[j][c + 1]);
-                            const float other = __shfl_xor_sync(0xFFFFFFFFu, gate ? d : a, 16);
-                            if (mine & (1u << c))
-                                y[static_cast<size_t>(64 * pass + 32 * j + c) * p.n] =
-                                    __float2half_rn(silu_mul_fast(gate ? a : other, gate ? other : d));
+                        for (int c8 = 0; c8 < 32; c8 += 8) {
+                            if ((stored >> c8 & 0xFFu) == 0u) continue;   // eight columns without a pair
+#pragma unroll
+                            for (int c = c8; c < c8 + 8; c += 2) {
+                                const float a = __uint_as_float(acc[j][c]), d = __uint_as_float(acc[j][c + 1]);
+                                const float other = __shfl_xor_sync(0xFFFFFFFFu, gate ? d : a, 16);
+                                if (mine & (1u << c))
+                                    y[static_cast<size_t>(64 * pass + 32 * j + c) * p.n] =
+                                        __float2half_rn(silu_mul_fast(gate ? a : other, gate ? other : d));
+                            }
                         }
                     }
                 }
