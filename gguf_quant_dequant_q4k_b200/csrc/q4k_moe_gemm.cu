@@ -85,7 +85,7 @@ struct MoeShape {
     static constexpr int slots = !WIDE ? 128 : SWIGLU ? 256 : 192;   // most slots per tile: MMA N
     static constexpr int d_bufs = WIDE ? 1 : 2;
     static constexpr int a_col0 = slots * d_bufs;            // TMEM: D, then A
-    static constexpr int a_bufs = 8;                         // decoded groups: four steps
+    static constexpr int a_steps = 4;                        // decoded steps
     static constexpr int sets = 3;
     static constexpr int epi_warp0 = kDecodeWarp0 + 4 * sets;
     static constexpr int threads = 32 * (epi_warp0 + 8);
@@ -98,8 +98,8 @@ struct MoeShape {
     static_assert(threads * regs_launch <= 65536 &&
                       128 * regs_copy + 128 * sets * regs_decode + 256 * regs_epi <= threads * regs_launch,
                   "register split");
-    static_assert(a_col0 + a_bufs * kGroup / 2 <= kMoeTmemCols, "TMEM");
-    static_assert(b_stages >= a_bufs / 2, "a step's barrier is reused behind its A buffers");
+    static_assert(a_col0 + a_steps * kStep / 2 <= kMoeTmemCols, "TMEM");
+    static_assert(b_stages >= a_steps, "a step's barrier is reused behind its A buffers");
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");
 };
 // At most this many pairs per expert on average: narrow. (Measured at 512 pairs per
@@ -178,33 +178,37 @@ struct QuantGroup {
     float s0, c0, s1, c1;   // 2^24 d sc_2g, -dmin m_2g, 2^20 d sc_2g+1, -dmin m_2g+1
 };
 
-// A superblock header as the groups use it: the six-bit fields of a word become
-// f32 as binary16 subnormals (times 2^-24), so the powers of two go to d, dmin.
-struct GroupHeader {
-    uint32_t sc_lo, sc_hi, m_lo, m_hi;
+// Half a superblock header, for the two groups of a step: the six-bit fields of
+// a word become f32 as binary16 subnormals (times 2^-24), so the powers of two go
+// to d, dmin.
+struct StepHeader {
+    uint32_t sc, mn;        // four sub-blocks' fields, a byte each
     float d48, d44, m24;    // 2^48 d, 2^44 d, -2^24 dmin (exact)
 
-    __device__ __forceinline__ void load(const uint8_t* src) {
-        const Header h = decode_header(*reinterpret_cast<const uint4*>(src));
-        sc_lo = h.sc_lo;
-        sc_hi = h.sc_hi;
-        m_lo = h.m_lo;
-        m_hi = h.m_hi;
-        d48 = h.d * 281474976710656.f;
-        d44 = h.d * 17592186044416.f;
-        m24 = h.dmin * -16777216.f;
+    __device__ __forceinline__ void load(const uint8_t* block, bool second) {
+        const uint4 h = *reinterpret_cast<const uint4*>(block);
+        const float2 d = widen_half2(h.x);
+        if (second) {
+            sc = (h.w & 0x0F0F0F0Fu) | (h.y >> 2 & 0x30303030u);
+            mn = (h.w >> 4 & 0x0F0F0F0Fu) | (h.z >> 2 & 0x30303030u);
+        } else {
+            sc = h.y & 0x3F3F3F3Fu;
+            mn = h.z & 0x3F3F3F3Fu;
+        }
+        d48 = d.x * 281474976710656.f;
+        d44 = d.x * 17592186044416.f;
+        m24 = d.y * -16777216.f;
     }
-    __device__ __forceinline__ QuantGroup group(const uint8_t* src, uint32_t g) const {
+    __device__ __forceinline__ QuantGroup group(const uint8_t* quants, bool second) const {
         QuantGroup r;
-        r.q0 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g);
-        r.q1 = *reinterpret_cast<const uint4*>(src + kQsOffset + 32 * g + 16);
-        const uint32_t pick = (g & 1u) != 0u ? 0x4342u : 0x4140u;   // bytes 2 (g & 1) and the next, widened to 16 bits
-        const float2 sc = widen_half2(__byte_perm(g < 2 ? sc_lo : sc_hi, 0u, pick));
-        const float2 mn = widen_half2(__byte_perm(g < 2 ? m_lo : m_hi, 0u, pick));
-        r.s0 = d48 * sc.x;
-        r.s1 = d44 * sc.y;
-        r.c0 = m24 * mn.x;
-        r.c1 = m24 * mn.y;
+        r.q0 = *reinterpret_cast<const uint4*>(quants);
+        r.q1 = *reinterpret_cast<const uint4*>(quants + 16);
+        const uint32_t pick = second ? 0x4342u : 0x4140u;   // two bytes, widened to 16 bits
+        const float2 s = widen_half2(__byte_perm(sc, 0u, pick)), m = widen_half2(__byte_perm(mn, 0u, pick));
+        r.s0 = d48 * s.x;
+        r.s1 = d44 * s.y;
+        r.c0 = m24 * m.x;
+        r.c1 = m24 * m.y;
         return r;
     }
 };
@@ -253,10 +257,10 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         sh.abort = 0;
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(&sh.w_full[i], 1);
-            mbar_init(&sh.w_empty[i], 4 * S::sets);        // decode warps
+            mbar_init(&sh.w_empty[i], 8);                // its two steps' decode warps
         }
         for (int i = 0; i < kBStages; ++i) {
-            mbar_init(&sh.full[i], 17);                  // B's bytes; two groups' decode warps in both CTAs
+            mbar_init(&sh.full[i], 9);                   // B's bytes; the step's decode warps in both CTAs
             mbar_init(&sh.done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -373,7 +377,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                                 s = 0;
                                 par ^= 1u;
                             }
-                            if (++abuf == S::a_bufs / 2) abuf = 0;
+                            if (++abuf == S::a_steps) abuf = 0;
                         }
                     }
                 }
@@ -425,9 +429,10 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         }
     } else if (warp < S::epi_warp0) {
         // ---------------------------------------------------- decode
-        // The pair's quant groups in the order of its tiles are numbered
-        // through: group i is decoded by set i % sets into TMEM buffer i % a_bufs
-        // for step i / 2.
+        // The pair's steps in the order of its tiles are numbered through: step i,
+        // two quant groups of a superblock, is decoded by set i % sets into TMEM
+        // buffer i % a_steps. (A set per group instead: three headers in four groups
+        // and twice the barriers; 777 tokens 109 us.)
         regs_lower<S::regs_decode>();
         const int quarter = warp & 3;
         const int row = SWIGLU ? (lane < 16 ? 0 : 64) + 16 * quarter + (lane & 15) : 32 * quarter + lane;
@@ -435,49 +440,48 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         const uint32_t full0 = map_to_rank(&sh.full[0], 0);
         const int pairs = static_cast<int>(gridDim.x >> 1), pair = static_cast<int>(blockIdx.x >> 1);
         const int tiles = sh.tile0[experts] > pair ? (sh.tile0[experts] - pair - 1) / pairs + 1 : 0;
-        const uint32_t groups = 4u * static_cast<uint32_t>(tiles) * static_cast<uint32_t>(nsb);
-        uint32_t have = ~0u;                 // superblock whose header is in hd
-        GroupHeader hd{};
+        const uint32_t steps = 2u * static_cast<uint32_t>(tiles) * static_cast<uint32_t>(nsb);
+        StepHeader hd;
         bool ok = true;
-        auto fetch = [&](uint32_t i) {       // group i's quants and factors
-            const uint32_t b = i >> 2, ws = b % kWStages;
-            const uint8_t* src = sw + ws * kWStageBytes + row * kBlockBytes;
-            if (b != have) {
-                ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], (b / kWStages) & 1u));
-                if (!ok) return QuantGroup{};
-                hd.load(src);
-                have = b;
-            }
-            const QuantGroup q = hd.group(src, i & 3u);
-            if ((i + S::sets) >> 2 != b) {   // this warp's last group of the superblock
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.w_empty[ws]);
-            }
-            return q;
+        const uint8_t* quants;
+        auto fetch = [&](uint32_t i) {       // step i's header, its first group's quants and factors
+            const uint32_t b = i >> 1, ws = b % kWStages;
+            const uint8_t* block = sw + ws * kWStageBytes + row * kBlockBytes;
+            ok = __all_sync(0xFFFFFFFFu, moe_wait(&sh.w_full[ws], (b / kWStages) & 1u));
+            if (!ok) return QuantGroup{};
+            hd.load(block, (i & 1u) != 0u);
+            quants = block + kQsOffset + ((i & 1u) != 0u ? 64 : 0);
+            return hd.group(quants, false);
         };
         uint32_t i = (warp - kDecodeWarp0) >> 2;
         QuantGroup q{};
-        if (i < groups) q = fetch(i);
+        if (i < steps) q = fetch(i);
 #pragma unroll 1
-        for (; ok && i < groups; i += S::sets) {
+        for (; ok && i < steps; i += S::sets) {
             // the buffer's last step: its barrier is polled ahead of the decoding, which covers the poll's latency
-            const uint32_t step = (i - S::a_bufs) >> 1;
-            uint64_t* free_bar = &sh.done[step % kBStages];
-            const uint32_t free_par = (step / kBStages) & 1u;
-            const bool free = i < S::a_bufs || mbar_try_wait_now(free_bar, free_par);
+            const uint32_t last = i - S::a_steps;
+            uint64_t* free_bar = &sh.done[last % kBStages];
+            const uint32_t free_par = (last / kBStages) & 1u;
+            const bool free = i < S::a_steps || mbar_try_wait_now(free_bar, free_par);
+            const uint32_t addr = lane_addr + (i % S::a_steps) * (kStep / 2);
             uint32_t r[32];
             decode_group(q, r);
+            q = hd.group(quants + 32, true);
             if (!__all_sync(0xFFFFFFFFu, free)) {
                 ok = __all_sync(0xFFFFFFFFu, moe_wait(free_bar, free_par));
                 if (!ok) break;
             }
             tc_fence_after_sync();
-            tmem_store_32cols(lane_addr + (i % S::a_bufs) * (kGroup / 2), r);
-            if (i + S::sets < groups) q = fetch(i + S::sets);
+            tmem_store_32cols(addr, r);
+            decode_group(q, r);
+            tmem_store_32cols(addr + kGroup / 2, r);
+            __syncwarp();                    // the superblock's quants are read
+            if (lane == 0) mbar_arrive(&sh.w_empty[(i >> 1) % kWStages]);
+            if (i + S::sets < steps) q = fetch(i + S::sets);
             tmem_wait_st();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(full0 + 8 * ((i >> 1) % kBStages));
+            if (lane == 0) mbar_arrive_cluster(full0 + 8 * (i % kBStages));
         }
         if (!ok) *abort_flag = 1;
     } else {
