@@ -12,12 +12,12 @@
 //   tiles of all experts, the blocks of a row tile one after another.
 // * A (weights). A producer streams 128 rows x 144 bytes per superblock into a
 //   shared-memory ring (TMA). Three sets of four decode warps (a warp per TMEM
-//   lane quarter, a lane per row) take the 64-weight quant groups in turn: the
-//   quants become f32 through binary16 subnormals, the weight is one packed fma,
-//   rounded once, then cvt to fp16 pairs, stored to TMEM. The decoded group
-//   feeds all N slots: a step's MMAs take 4 N cycles, its decoding about 950
-//   (408 issue slots on each SM sub-partition without any wait), so blocks of
-//   about 230 slots and more hide it.
+//   lane quarter, a lane per row) take the steps (two 64-weight quant groups) in
+//   turn: the quants become f32 through binary16 subnormals, the weight is one
+//   packed fma, rounded once, then cvt to fp16 pairs, stored to TMEM. The decoded
+//   step feeds all N slots: its MMAs take 4 N cycles, at least 390 (reading A),
+//   its decoding about 750 (500 on an SM that does nothing else), so blocks of
+//   about 190 slots and more hide it.
 // * B (activations). 128 elements of N / 2 rows per CTA and step, by TMA in the
 //   128-byte-swizzled layout; the pair's tensor cores share the two halves. x
 //   in slot order is read in place; otherwise a copy in slot order is made
@@ -32,10 +32,11 @@
 // * Measured (times are of calls back to back; the clock falls to about 1.5 GHz
 //   under the large cases): 2048 tokens, 8 experts, top 2: gate/up 14336 x 4096
 //   0.82-0.93 ms = 1030-1170 TFLOP/s (cuBLAS bf16, sustained: 1428), bound by
-//   the MMAs, 1126 cycles per step of about 910; down 4096 x 14336 0.49-0.56 ms,
+//   the MMAs, 1088 cycles per step of about 910; down 4096 x 14336 0.49-0.56 ms,
 //   bound by the decoding and the drains of D. 777 tokens, 64 experts, top 4
-//   (about 48 slots each): gate/up 1536 x 2048 112-128 us, down 62-67 us, bound
-//   by the decoding (975 cycles per step).
+//   (about 48 slots each): gate/up 1536 x 2048 100 us, down 55 us, bound by the
+//   decoding (785 cycles per step, issue slots 0.67; without the arithmetic of
+//   the decoding, to see the rest: 624).
 // * Waits are bounded; a role that gives up raises Q4K_FAULT_COPY_TIMEOUT and
 //   the CTA lets its copies and MMAs land before shared memory and TMEM go.
 #include <cstdint>

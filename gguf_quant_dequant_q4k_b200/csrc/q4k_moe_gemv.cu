@@ -21,18 +21,20 @@
 //   the bytes 8 t .. 8 t + 7 of each 32-byte quant group (a permutation of K
 //   inside the sub-block that the digit image repeats). Rows 288 bytes apart
 //   make those 8-byte loads free of bank conflicts.
-// * Work. A unit is 16 rows x one group of vectors; clusters of CTAs own equal
-//   contiguous ranges of units, the CTAs of a cluster equal parts of K (one CTA
-//   where the digit image of the whole row fits), the warps of a CTA equal
-//   ranges of the (unit, box) items of a round. With one CTA per cluster a
-//   round is all its units of a group: a warp stores the units it has whole, and
-//   the units cut between warps (at most one per warp) meet in shared memory.
-//   With several, a round is up to kRoundUnits units and all pieces meet in the
-//   cluster's shared memory. Pieces are added in a fixed order.
-// * Bound and measured. One token, 8 experts, top 2: gate/up 14336 x 4096 35 us
-//   (3.8 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 21
-//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 53-58 us, down 28-32
-//   us. Of the one-token call about 6 us are its start (planning, digits, the
+// * Work. A unit is 16 rows x one group of vectors; clusters of CTAs own
+//   contiguous ranges of units of equal cost (a group of three or four vectors
+//   is two columns of MMAs and costs half as much again as one of two: 24 tokens
+//   56 -> 52 us and 31 -> 29), the CTAs of a cluster equal parts of K (one CTA
+//   where the digit image of the whole row fits), the warps of a CTA equal ranges
+//   of the (unit, box) items of a round. With one CTA per cluster a round is all
+//   its units of a group: a warp stores the units it has whole, and the units cut
+//   between warps (at most one per warp) meet in shared memory. With several, a
+//   round is up to kRoundUnits units and all pieces meet in the cluster's shared
+//   memory. Pieces are added in a fixed order.
+// * Bound and measured. One token, 8 experts, top 2: gate/up 14336 x 4096 34 us
+//   (3.9 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 21
+//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 52 us, down 29 us.
+//   Of the one-token call about 6 us are its start (planning, digits, the
 //   first boxes), the loop runs at 0.58 of the issue slots; with three or four
 //   vectors per group the issue slots set the pace.
 #include <cstdint>
@@ -60,6 +62,7 @@ constexpr int kVBoxCols = 2;                      // superblocks per box
 constexpr int kVRowPitch = kVBoxCols * kBlockBytes;
 constexpr int kVBoxBytes = kVRows * kVRowPitch;
 constexpr int kVMaxVec = 4;                       // vectors per group
+constexpr int kCost2 = 2, kCost4 = 3;             // of a unit of up to two, and of four vectors
 constexpr int kRoundUnits = 16;                   // most units of a round in a cluster of several CTAs
 // Pieces of units in shared memory. Several CTAs: every piece of a round,
 // numbered unit + warp (unique: of two neighbouring pieces one or both grow).
@@ -102,11 +105,16 @@ struct GemvShared {   // static: below the 6 KB that kVSmemLimit leaves
     uint64_t full[kVWarps][kVStages];
     int chunk0[Q4K_MOE_MAX_EXPERTS + 1];            // first vector group of each expert
     int first[Q4K_MOE_MAX_EXPERTS], count[Q4K_MOE_MAX_EXPERTS];
-    int order[kVThreads];                           // of the first pairs
+    int cost0[Q4K_MOE_MAX_EXPERTS + 1];             // cost of a row tile of all groups before the expert's
+    short order[kVThreads];                         // of the first pairs; -1: out of range
     long long range[2];
     int head[kVWarps];                              // rounds whose head piece the warp has left, plus one
     int abort;
 };
+
+// What a unit of an expert's groups costs: three or four vectors are two columns
+// of MMAs.
+__device__ __forceinline__ int unit_cost(int cnt, int chunks) { return cnt > 2 * chunks ? kCost4 : kCost2; }
 
 // d = A B^T: A 16 x 32 unsigned bytes (a0, a2: row g, a1, a3: row g + 8), B 8 x 32 signed.
 static_assert(sizeof(GemvShared) <= 6144 - 256, "shared memory");
@@ -135,6 +143,15 @@ __device__ __forceinline__ int dp2a_hi(int a, uint32_t b, int c) {
 // A 32-bit integer as f64, exactly: 2^52 + 2^31 + v less 2^52 + 2^31.
 __device__ __forceinline__ double int_to_f64(int v) {
     return __hiloint2double(0x43300000, v ^ static_cast<int>(0x80000000u)) - 4503601774854144.0;
+}
+
+// a + 256 b as f64, exactly: as a 64-bit integer added to the bits of 2^52 + 2^51.
+__device__ __forceinline__ double digits_to_f64(int a, int b) {
+    const long long base = static_cast<long long>(static_cast<unsigned long long>(static_cast<uint32_t>(0x43380000 + (a >> 31))) << 32 |
+                                                  static_cast<uint32_t>(a));
+    long long v;
+    asm("mad.wide.s32 %0, %1, 256, %2;" : "=l"(v) : "r"(b), "l"(base));
+    return __longlong_as_double(v) - 6755399441055744.0;
 }
 
 // The digits of one vector's block (lane: K positions 8 lane .. + 7, v). E is
@@ -205,8 +222,8 @@ __device__ __forceinline__ void superblock_rows(const uint8_t* rows, const uint8
         const uint2 qa = *reinterpret_cast<const uint2*>(ra + kQsOffset + 32 * jp + 8 * t);
         const uint2 qb = *reinterpret_cast<const uint2*>(rb + kQsOffset + 32 * jp + 8 * t);
         const uint32_t wa = jp < 2 ? ha.sc_lo : ha.sc_hi, wb = jp < 2 ? hb.sc_lo : hb.sc_hi;
-        const int sae = static_cast<int>(16u * byte_of(wa, (2 * jp) & 3)), sao = static_cast<int>(byte_of(wa, (2 * jp + 1) & 3));
-        const int sbe = static_cast<int>(16u * byte_of(wb, (2 * jp) & 3)), sbo = static_cast<int>(byte_of(wb, (2 * jp + 1) & 3));
+        const int sae = static_cast<int>(__byte_perm(wa, 0u, 0x4440u + ((2 * jp) & 3)) << 4), sao = static_cast<int>(__byte_perm(wa, 0u, 0x4440u + ((2 * jp + 1) & 3)));
+        const int sbe = static_cast<int>(__byte_perm(wb, 0u, 0x4440u + ((2 * jp) & 3)) << 4), sbo = static_cast<int>(__byte_perm(wb, 0u, 0x4440u + ((2 * jp + 1) & 3)));
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const uint4 dg = *reinterpret_cast<const uint4*>(sb_image + i * kVImageBytes + jp * 512 + lane * 16);
@@ -237,8 +254,8 @@ __device__ __forceinline__ void superblock_rows(const uint8_t* rows, const uint8
         const int m_a = mins(s0, ha.m_lo, ha.m_hi) + 256 * mins(s1, ha.m_lo, ha.m_hi);
         const int m_b = mins(s0, hb.m_lo, hb.m_hi) + 256 * mins(s1, hb.m_lo, hb.m_hi);
         // |16 P_l| <= 16 * 8 * 63 * 32 * 15 * 128 < 2^29
-        const double pa = fma(256.0, int_to_f64(ps[i][1]), int_to_f64(ps[i][0]));
-        const double pb = fma(256.0, int_to_f64(ps[i][3]), int_to_f64(ps[i][2]));
+        const double pa = digits_to_f64(ps[i][0], ps[i][1]);
+        const double pb = digits_to_f64(ps[i][2], ps[i][3]);
         acc[i][0] = fma(scale, fma(da, pa, ma * int_to_f64(m_a)), acc[i][0]);
         acc[i][1] = fma(scale, fma(db, pb, mb * int_to_f64(m_b)), acc[i][1]);
     }
@@ -282,12 +299,16 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     pdl_launch_dependents();
     pdl_wait();
     // Experts' slots and first vector groups (warp 0; the others' redundant scans would fill the issue slots).
-    if (threadIdx.x < p.g.pairs) sh.order[threadIdx.x] = __ldg(p.g.order + threadIdx.x);
+    if (threadIdx.x < p.g.pairs) {
+        const int v = __ldg(p.g.order + threadIdx.x);
+        sh.order[threadIdx.x] = static_cast<short>(v >= 0 && v < p.g.pairs ? v : -1);
+    }
     if (warp == 0) {
-        int before = 0;
+        const bool even = p.cap == 2;         // every unit costs the same
+        int chunks_before = 0, cost_before = 0;
         for (int e0 = 0; e0 < experts; e0 += 32) {
             const int e = e0 + lane;
-            int chunks = 0;
+            int chunks = 0, cost = 0;
             if (e < experts) {
                 const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
                 const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
@@ -295,7 +316,8 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 const int cnt = ok ? b - a : 0;
                 sh.first[e] = a;
                 sh.count[e] = cnt;
-                chunks = (cnt + p.cap - 1) >> (p.cap == 4 ? 2 : 1);
+                chunks = (cnt + p.cap - 1) >> (even ? 1 : 2);
+                cost = chunks * unit_cost(cnt, chunks);
             }
             int scan = chunks;
 #pragma unroll
@@ -303,16 +325,46 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 const int v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
                 if (lane >= off) scan += v;
             }
-            if (e < experts) sh.chunk0[e + 1] = before + scan;
-            before += __shfl_sync(0xFFFFFFFFu, scan, 31);
+            if (e < experts) sh.chunk0[e + 1] = chunks_before + scan;
+            chunks_before += __shfl_sync(0xFFFFFFFFu, scan, 31);
+            if (!even) {
+                scan = cost;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int v = __shfl_up_sync(0xFFFFFFFFu, scan, off);
+                    if (lane >= off) scan += v;
+                }
+                if (e < experts) sh.cost0[e + 1] = cost_before + scan;
+                cost_before += __shfl_sync(0xFFFFFFFFu, scan, 31);
+            }
         }
-        if (lane < 2) {              // this cluster's units: [range[0], range[1])
-            const long long all = static_cast<long long>(before) * p.units;
-            sh.range[lane] = all < (1 << 23)   // at most 148 clusters: 32-bit division
-                                 ? static_cast<long long>(static_cast<uint32_t>(all) * (cid + lane) / nclusters)
-                                 : all * (cid + lane) / nclusters;
+        if (lane == 0) sh.chunk0[0] = sh.cost0[0] = 0;
+        __syncwarp();
+        // This cluster's units, [range[0], range[1]): an equal share of the cost.
+        const long long total = static_cast<long long>(even ? chunks_before : cost_before) * p.units;
+        auto share = [&](int i) {
+            return total < (1 << 23)          // at most 148 clusters: 32-bit division
+                       ? static_cast<long long>(static_cast<uint32_t>(total) * (cid + i) / nclusters)
+                       : total * (cid + i) / nclusters;
+        };
+        if (even) {
+            if (lane < 2) sh.range[lane] = share(lane);
+        } else {
+            // a bound lies in the expert whose costs it falls into, or behind them all; neighbours find the same one
+            const long long bound[2] = {share(0), share(1)};
+            if (lane < 2 && bound[lane & 1] >= total) sh.range[lane] = static_cast<long long>(chunks_before) * p.units;
+            for (int e = lane; e < experts; e += 32) {
+                const int c0 = sh.chunk0[e], each = unit_cost(sh.count[e], sh.chunk0[e + 1] - c0);
+                const long long lo = static_cast<long long>(sh.cost0[e]) * p.units;
+                const long long hi = static_cast<long long>(sh.cost0[e + 1]) * p.units;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (bound[i] < lo || bound[i] >= hi) continue;
+                    const long long in = bound[i] - lo;
+                    sh.range[i] = static_cast<long long>(c0) * p.units + (each == kCost2 ? in / kCost2 : in / kCost4);
+                }
+            }
         }
-        if (lane == 0) sh.chunk0[0] = 0;
     }
     __syncthreads();
     const long long u0 = sh.range[0], u1 = sh.range[1];
