@@ -26,14 +26,14 @@
 //   is two columns of MMAs and costs half as much again as one of two: 24 tokens
 //   56 -> 52 us and 31 -> 29), the CTAs of a cluster equal parts of K (one CTA
 //   where the digit image of the whole row fits), the warps of a CTA equal ranges
-//   of the (unit, box) items of a round. With one CTA per cluster a round is all
+//   of the columns of a round's units. With one CTA per cluster a round is all
 //   its units of a group: a warp stores the units it has whole, and the units cut
 //   between warps (at most one per warp) meet in shared memory. With several, a
 //   round is up to kRoundUnits units and all pieces meet in the cluster's shared
 //   memory. Pieces are added in a fixed order.
-// * Bound and measured. One token, 8 experts, top 2: gate/up 14336 x 4096 34 us
-//   (3.9 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 21
-//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 52 us, down 29 us.
+// * Bound and measured. One token, 8 experts, top 2: gate/up 14336 x 4096 33 us
+//   (4.0 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 21
+//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 50 us, down 29 us.
 //   Of the one-token call about 6 us are its start (planning, digits, the
 //   first boxes), the loop runs at 0.58 of the issue slots; with three or four
 //   vectors per group the issue slots set the pace.
@@ -284,7 +284,10 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const int experts = p.g.experts;
     const int sb0 = static_cast<int>(rank) * p.part_sbs;
     const int sbs = max(0, min(p.part_sbs, p.nsb - sb0));  // this CTA's superblocks
-    const int boxes = (p.part_sbs + kVBoxCols - 1) / kVBoxCols;   // per unit and matrix, the same in every CTA
+    // The warps' shares are counted in columns of kItem superblocks: of one for two matrices (24 tokens: 52 -> 50 us),
+    // of a box for one matrix (half boxes: 28.5 -> 29.5 us). Columns per unit, the same in every CTA:
+    constexpr int kItem = SWIGLU ? 1 : kVBoxCols;
+    const int cols = (p.part_sbs + kItem - 1) / kItem;
 
     if (lane == 0) {
         for (int s = 0; s < kVStages; ++s) mbar_init(&sh.full[warp][s], 1);
@@ -387,7 +390,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         return r;
     };
     auto item_begin = [&](int count, int w) {
-        return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(count) * static_cast<uint32_t>(boxes)) *
+        return static_cast<int>(static_cast<unsigned long long>(static_cast<uint32_t>(count) * static_cast<uint32_t>(cols)) *
                                 static_cast<uint32_t>(w) / kVWarps);
     };
     const int piece = v_piece_doubles(p.cap, SWIGLU);
@@ -395,12 +398,14 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     // This warp's boxes in order, requested kVStages ahead of use.
     const Round first_round = open_round(u0, 0);
     Round pr = first_round;
-    int p_left = 0, p_box = 0, p_row = 0, p_mat = 0, p_stage = 0;   // items left in the round, the next one's box and row
+    int p_left = 0, p_col = 0, p_row = 0, p_mat = 0, p_stage = 0;   // columns left in the round, the next one and its row
+    // Columns of the box that starts at col: up to the unit's or the range's end.
+    auto box_cols = [&](int col, int left) { return min(min(kVBoxCols / kItem, cols - col), left); };
     auto enter = [&] {
         const int i0 = item_begin(pr.count, warp);
         p_left = item_begin(pr.count, warp + 1) - i0;
-        const int unit = i0 / boxes;
-        p_box = i0 - unit * boxes;
+        const int unit = i0 / cols;
+        p_col = i0 - unit * cols;
         p_row = pr.e * p.n + (pr.tile + unit) * kVRows;
     };
     enter();
@@ -413,13 +418,15 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         if (lane == 0) {
             mbar_arrive_expect_tx(&sh.full[warp][p_stage], kVBoxBytes);
             tma_load_3d(ring + (warp * kVStages + p_stage) * kVBoxBytes, p_mat == 0 ? &map_w : &map_w2, 0,
-                        sb0 + p_box * kVBoxCols, p_row, &sh.full[warp][p_stage]);
+                        sb0 + p_col * kItem, p_row, &sh.full[warp][p_stage]);
         }
         if (++p_mat == R) {
             p_mat = 0;
-            --p_left;
-            if (++p_box == boxes) {
-                p_box = 0;
+            const int take = box_cols(p_col, p_left);
+            p_left -= take;
+            p_col += take;
+            if (p_col == cols) {
+                p_col = 0;
                 p_row += kVRows;
             }
         }
@@ -521,11 +528,12 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             constexpr int NT = decltype(nt_tag)::value;
             // totals of the matrix at hand and of the other one (swapped after every box: one copy of the loop's code)
             double acc[NT][2], other[NT][2];
-            int unit = i0 / boxes, box = i0 - unit * boxes;
-            bool whole = true;       // the piece starts at its unit's first box
-            for (int it = i0; it < i1 && ok; ++it) {
-                if (it == i0 || box == 0) {
-                    whole = box == 0;
+            int unit = i0 / cols, col = i0 - unit * cols;
+            bool whole = true;       // the piece starts at its unit's first superblock
+            for (int it = i0; it < i1 && ok;) {
+                const int take = box_cols(col, i1 - it);
+                if (it == i0 || col == 0) {
+                    whole = col == 0;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = other[i][0] = other[i][1] = 0.0;
                 }
@@ -537,9 +545,8 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (!ok) break;
                     const uint8_t* rows = ring + (warp * kVStages + stage) * kVBoxBytes;
 #pragma unroll 1
-                    for (int b = box * kVBoxCols; b < min(sbs, (box + 1) * kVBoxCols); ++b)
-                        superblock_rows<NT>(rows + (b & (kVBoxCols - 1)) * kBlockBytes, image + b * sb_bytes, meta_offset, lane,
-                                            acc);
+                    for (int b = 0; b < min(take * kItem, sbs - col * kItem); ++b)
+                        superblock_rows<NT>(rows + b * kBlockBytes, image + (col * kItem + b) * sb_bytes, meta_offset, lane, acc);
                     __syncwarp();              // every lane has read the box
                     request();
                     if (++stage == kVStages) {
@@ -557,8 +564,10 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                             }
                     }
                 }
-                const bool ends = box + 1 == boxes;
-                if (ok && (ends || it + 1 == i1)) {    // the piece of this unit
+                it += take;
+                col += take;
+                const bool ends = col == cols;
+                if (ok && (ends || it == i1)) {        // the piece of this unit
                     if (!parts_free) {
                         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
                         parts_free = true;
@@ -569,7 +578,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     const bool head = csize > 1 || !whole;     // goes to shared memory
                     double* out = parts + static_cast<size_t>(csize > 1 ? unit + warp : warp) * piece + row;
                     if (csize == 1 && whole && !ends) {        // the rest of the unit: the next warps' heads
-                        for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
+                        for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * cols; ++w)
                             if (item_begin(r.count, w) < item_begin(r.count, w + 1)) ok = wait_head(w, round_no) && ok;
                     }
 #pragma unroll
@@ -586,7 +595,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         const int pair = __shfl_sync(0xFFFFFFFFu, my_pair, vec);
                         if (!head) {
                             if (!ends)
-                                for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * boxes; ++w)
+                                for (int w = warp + 1; w < kVWarps && item_begin(r.count, w) < (unit + 1) * cols; ++w)
                                     if (item_begin(r.count, w) < item_begin(r.count, w + 1)) {
 #pragma unroll
                                         for (int m = 0; m < R; ++m)
@@ -600,8 +609,8 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         if (lane == 0) publish_head(round_no);
                     }
                 }
-                if (++box == boxes) {
-                    box = 0;
+                if (ends) {
+                    col = 0;
                     ++unit;
                 }
             }
@@ -621,13 +630,13 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             cluster_sync();
             const bool sound = *static_cast<volatile int*>(&sh.abort) == 0;
             // Totals: thread = (unit, vector, row), the cluster's CTAs take alternate units; pieces in order of CTA and warp.
-            const int items = r.count * boxes;
+            const int items = r.count * cols;
             for (int i = threadIdx.x; i < r.count * p.cap * kVRows; i += kVThreads) {
                 const int unit = i / (p.cap * kVRows), v = i / kVRows % p.cap, row = i % kVRows;
                 if (unit % csize != rank || v >= vecs || !sound) continue;
                 const int pair = __ldg(p.g.order + slot0 + v);
                 // the warps whose items touch the unit
-                const int wa = ((unit * boxes + 1) * kVWarps - 1) / items, wb = ((unit + 1) * boxes * kVWarps - 1) / items;
+                const int wa = ((unit * cols + 1) * kVWarps - 1) / items, wb = ((unit + 1) * cols * kVWarps - 1) / items;
                 double sum[2] = {0.0, 0.0};
                 for (uint32_t cta = 0; cta < csize; ++cta)
                     for (int w = wa; w <= wb; ++w) {
