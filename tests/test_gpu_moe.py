@@ -229,6 +229,18 @@ def test_gemv_long_rows_in_slot_order(q4k, mats):
     check_product(p, run_product(q4k, p), "long rows")
 
 
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("n,k", [(600, 1792), (2600, 256), (40, 512), (300, 14336)])
+def test_gemv_uneven_groups(q4k, n, k, mats):
+    """Experts of no, one to five, nine and seventeen vectors: groups of unequal cost shared out to the clusters,
+    rows of an odd number of superblocks cut between warps; every row of every pair is written."""
+    counts = [0, 5, 1, 0, 17, 2, 3, 9, 4, 0]
+    ids = np.repeat(np.arange(10), counts).astype(np.int32)
+    ids = np.random.default_rng(5).permutation(ids).reshape(-1, 1)
+    p = Problem(len(ids), 10, 1, n, k, 82 + n, mats=mats, ids=ids)
+    check_product(p, run_product(q4k, p), f"{n}x{k}")
+
+
 @pytest.mark.parametrize("half", [False, True])
 @pytest.mark.parametrize("mats", [1, 2])
 @pytest.mark.parametrize("k", [512, 14336])
