@@ -37,11 +37,11 @@ constexpr int kGroupBatch = 8;       // ids per lane in flight
 constexpr int kSmallTokens = 64;     // two tokens per warp of the one CTA
 static_assert(kSmallTokens * Q4K_MOE_MAX_TOP_K <= 1024, "one pass of 32 pairs per warp");
 
-// Larger float, larger key; NaN and -inf get 0 (never chosen), +inf the key of
-// FLT_MAX.
+// Larger float, larger key; equal floats, equal keys (-0.0 + 0.0 is +0.0); NaN
+// and -inf get 0 (never chosen), +inf the key of FLT_MAX.
 __device__ __forceinline__ uint32_t logit_key(float v) {
     if (!(v > -INFINITY)) return 0u;
-    const uint32_t b = __float_as_uint(fminf(v, FLT_MAX));
+    const uint32_t b = __float_as_uint(__fadd_rn(fminf(v, FLT_MAX), 0.0f));
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
