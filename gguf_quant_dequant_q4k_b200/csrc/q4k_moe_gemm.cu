@@ -608,9 +608,11 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     }
 }
 
-// out[s] = x[order[s] / per_row], s < offsets[experts]: a warp per row, four
-// 16-byte loads per lane in flight. A bad entry takes row 0 (the product does
-// not store its slot).
+// out[s] = x[order[s] / per_row] for every slot whose entry is a pair: a warp per
+// row, four 16-byte loads per lane in flight. All entries are looked at, not those
+// below offsets[experts]: where some expert's offsets are bad, another's slots may
+// lie behind that. A slot without a pair is not copied (the product does not store
+// it, and a column of B reaches no other column of D).
 constexpr int kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads)
@@ -618,13 +620,12 @@ q4k_moe_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, cons
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int slots = min(g.pairs, __ldg(g.offsets + g.experts));
     const int warps = static_cast<int>(gridDim.x) * (kGatherThreads / 32);
-    for (int s = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5); s < slots;
+    for (int s = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5); s < g.pairs;
          s += warps) {
         const int pair = __ldg(g.order + s);
-        const int row = pair >= 0 && pair < g.pairs ? pair / g.per_row : 0;
-        const uint4* src = x + static_cast<size_t>(row) * row16;
+        if (pair < 0 || pair >= g.pairs) continue;
+        const uint4* src = x + static_cast<size_t>(pair / g.per_row) * row16;
         uint4* dst = out + static_cast<size_t>(s) * row16;
         for (int c0 = lane; c0 < row16; c0 += 128) {
             uint4 v[4];
