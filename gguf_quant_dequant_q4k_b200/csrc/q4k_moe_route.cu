@@ -58,9 +58,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Token t's choices and weights, by one warp. S: keys per lane, experts <= 32 S.
 template <int S>
 __device__ __forceinline__ void choose_token(const float* __restrict__ logits, int* __restrict__ ids,
-                                             float* __restrict__ weights, int t, int n_experts, int top_k, bool renorm,
-                                             int lane) {
-    const float* row = logits + static_cast<size_t>(t) * n_experts;
+                                             float* __restrict__ weights, long long t, int n_experts, int top_k,
+                                             bool renorm, int lane) {
+    const float* row = logits + t * n_experts;
     uint32_t key[S];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
@@ -101,8 +101,8 @@ __device__ __forceinline__ void choose_token(const float* __restrict__ logits, i
     }
     const float total = renorm ? warp_sum(mine) : all;
     if (lane < top_k) {
-        ids[static_cast<size_t>(t) * top_k + lane] = chosen;
-        weights[static_cast<size_t>(t) * top_k + lane] = chosen >= 0 ? __fdiv_rn(mine, total) : 0.f;
+        ids[t * top_k + lane] = chosen;
+        weights[t * top_k + lane] = chosen >= 0 ? __fdiv_rn(mine, total) : 0.f;
     }
 }
 
@@ -215,7 +215,7 @@ q4k_moe_choose_kernel(const float* __restrict__ logits, int* __restrict__ ids, f
     const int lane = threadIdx.x & 31;
     const int warp0 = (blockIdx.x * kChooseThreads + threadIdx.x) >> 5;
     const int nwarps = (gridDim.x * kChooseThreads) >> 5;
-    for (int t = warp0; t < n_tokens; t += nwarps)
+    for (long long t = warp0; t < n_tokens; t += nwarps)   // 64-bit: n_tokens + nwarps may pass 2^31
         choose_token<S>(logits, ids, weights, t, n_experts, top_k, renorm, lane);
 }
 
@@ -266,7 +266,7 @@ cudaError_t launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
                                   a.n_tokens, a.n_experts, a.top_k, a.renorm);
     }
     const int per_cta = kChooseThreads / 32;
-    const int blocks = (a.n_tokens + per_cta - 1) / per_cta;
+    const long long blocks = (static_cast<long long>(a.n_tokens) + per_cta - 1) / per_cta;
     cfg.gridDim = dim3(static_cast<unsigned>(blocks < num_sms * 8 ? blocks : num_sms * 8));
     cfg.blockDim = dim3(kChooseThreads);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, q4k_moe_choose_kernel<S>, a.logits, a.ids, a.weights, a.n_tokens,

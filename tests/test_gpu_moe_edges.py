@@ -30,6 +30,39 @@ def test_route_signed_zeros_tie(q4k, t, e, top_k, renorm):
     base.check_route(base.gpu_route(q4k, logits, top_k, renorm), logits, top_k, renorm, f"{t}x{e} top {top_k}")
 
 
+def test_route_of_the_most_tokens(q4k):
+    """The largest batch the call accepts (2^31 - 1 tokens of one expert): token
+    indexes plus a grid's stride pass 2^31. Every 1000003rd token, and the last, has
+    no expert left."""
+    t, gap = 2 ** 31 - 1, 1000003
+    if torch.cuda.mem_get_info()[0] < 44e9:
+        pytest.skip("needs 44 GB of device memory")
+    logits = torch.zeros(t, device="cuda")
+    logits[::gap] = -float("inf")
+    logits[-1] = -float("inf")
+    ids, order = (torch.full((t,), 99, dtype=torch.int32, device="cuda") for _ in range(2))
+    w = torch.full((t,), 99.0, device="cuda")
+    off = torch.full((2,), 99, dtype=torch.int32, device="cuda")
+    q4k.q4k_moe_route(logits, ids, w, off, order, t, 1, 1)
+    torch.cuda.synchronize()
+    lost = torch.cat([torch.arange(0, t, gap, device="cuda"), torch.tensor([t - 1], device="cuda")])
+    live = t - lost.numel()
+    assert off.tolist() == [0, live]
+    slot0 = 0
+    for a in range(0, t, 2 ** 27):
+        b = min(a + 2 ** 27, t)
+        want = torch.zeros(b - a, dtype=torch.int32, device="cuda")
+        want[lost[(lost >= a) & (lost < b)] - a] = -1
+        assert torch.equal(ids[a:b], want)
+        assert torch.equal(w[a:b], (want + 1).float())
+        pairs = torch.nonzero(want == 0).view(-1) + a
+        assert torch.equal(order[slot0:slot0 + pairs.numel()].long(), pairs)
+        slot0 += pairs.numel()
+    assert slot0 == live and bool((order[live:] == -1).all())
+    del logits, ids, order, w, want, pairs
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ products
 
 def slot_rows(p, e, a, b):
