@@ -2,6 +2,12 @@
 // router (q4k_moe_route.cu), the expert-grouped Q4_K products
 // (q4k_moe_gemv.cu, q4k_moe_gemm.cu) and the weighted combination
 // (q4k_moe_combine.cu). Arguments are validated by the callers (q4k_api.cu).
+//
+// The kernels are launched programmatically and let their successors start before
+// their own wait for their predecessor: what an earlier kernel may write (logits,
+// ids, weights, offsets, order, x, z) is read by plain loads behind pdl_wait() (or
+// by TMA), never by non-coherent ones, which need data that nothing writes while
+// the grid lives; no pointer to it is const __restrict__.
 #pragma once
 
 #include <cuda_runtime.h>

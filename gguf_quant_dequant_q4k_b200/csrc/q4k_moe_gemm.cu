@@ -282,7 +282,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         int tiles = 0;
         const int e = threadIdx.x;
         if (e < experts) {
-            const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
+            const int a = p.g.offsets[e], b = p.g.offsets[e + 1];
             const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
             if (!ok && blockIdx.x == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
             const int cnt = ok ? b - a : 0;
@@ -503,7 +503,7 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                 const int c = c0 + 32 * j + lane;
                 pair[j] = -1;
                 if (c < t.slots) {
-                    const int v = __ldg(p.g.order + t.slot0 + c);
+                    const int v = p.g.order[t.slot0 + c];
                     if (v >= 0 && v < p.g.pairs) pair[j] = v;
                     else if (t.row_tile == 0) atomicOr(&g_moe_gemm_fault_flags, Q4K_FAULT_ROUTE_RANGE);
                 }
@@ -616,14 +616,14 @@ q4k_moe_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 constexpr int kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads)
-q4k_moe_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, const MoeGroups g, int row16) {
+q4k_moe_gather_kernel(const uint4* x, uint4* __restrict__ out, const MoeGroups g, int row16) {
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int warps = static_cast<int>(gridDim.x) * (kGatherThreads / 32);
     for (int s = static_cast<int>(blockIdx.x) * (kGatherThreads / 32) + static_cast<int>(threadIdx.x >> 5); s < g.pairs;
          s += warps) {
-        const int pair = __ldg(g.order + s);
+        const int pair = g.order[s];
         if (pair < 0 || pair >= g.pairs) continue;
         const uint4* src = x + static_cast<size_t>(pair / g.per_row) * row16;
         uint4* dst = out + static_cast<size_t>(s) * row16;
@@ -631,7 +631,7 @@ q4k_moe_gather_kernel(const uint4* __restrict__ x, uint4* __restrict__ out, cons
             uint4 v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (c0 + 32 * i < row16) v[i] = __ldg(src + c0 + 32 * i);
+                if (c0 + 32 * i < row16) v[i] = src[c0 + 32 * i];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (c0 + 32 * i < row16) dst[c0 + 32 * i] = v[i];

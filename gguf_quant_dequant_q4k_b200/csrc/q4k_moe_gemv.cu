@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "q4k_internal.h"
+#include "q4k_moe.cuh"
 #include "q4k_moe.h"
 #include "q4k_pair.cuh"
 #include "q4k_superblock.cuh"
@@ -302,18 +303,24 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     pdl_launch_dependents();
     pdl_wait();
     // Experts' slots and first vector groups (warp 0; the others' redundant scans would fill the issue slots).
-    if (threadIdx.x < p.g.pairs) {
-        const int v = __ldg(p.g.order + threadIdx.x);
-        sh.order[threadIdx.x] = static_cast<short>(v >= 0 && v < p.g.pairs ? v : -1);
-    }
+    // All first loads are requested before any is used: behind one another they take 0.7-1.5 us of a call.
+    const int my_order = threadIdx.x < p.g.pairs ? load_i32(p.g.order + threadIdx.x) : -1;
+    int2 bounds = make_int2(0, 0);                         // of expert `lane`, then of the next 32
+    auto load_bounds = [&](int e) {
+        return e < experts ? make_int2(load_i32(p.g.offsets + e), load_i32(p.g.offsets + e + 1)) : make_int2(0, 0);
+    };
+    if (warp == 0) bounds = load_bounds(lane);
+    if (threadIdx.x < p.g.pairs)
+        sh.order[threadIdx.x] = static_cast<short>(my_order >= 0 && my_order < p.g.pairs ? my_order : -1);
     if (warp == 0) {
         const bool even = p.cap == 2;         // every unit costs the same
         int chunks_before = 0, cost_before = 0;
         for (int e0 = 0; e0 < experts; e0 += 32) {
             const int e = e0 + lane;
             int chunks = 0, cost = 0;
+            const int a = bounds.x, b = bounds.y;
+            bounds = load_bounds(e + 32);
             if (e < experts) {
-                const int a = __ldg(p.g.offsets + e), b = __ldg(p.g.offsets + e + 1);
                 const bool ok = a >= 0 && a <= b && b <= p.g.pairs;
                 if (!ok && blockIdx.x == 0) atomicOr(&g_moe_gemv_fault_flags, Q4K_FAULT_ROUTE_RANGE);
                 const int cnt = ok ? b - a : 0;
@@ -450,7 +457,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         g.pair = -1;
         if (lane < g.vecs) {
             const int slot = g.slot0 + lane;
-            const int v = slot < kVThreads ? sh.order[slot] : __ldg(p.g.order + slot);
+            const int v = slot < kVThreads ? sh.order[slot] : p.g.order[slot];
             if (v >= 0 && v < p.g.pairs) g.pair = v;
         }
         return g;
@@ -463,7 +470,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         const int row = p.g.per_row == 0 ? g.slot0 + vec : pair >= 0 ? pair / p.g.per_row : 0;
         const float4* src =
             reinterpret_cast<const float4*>(p.x + static_cast<size_t>(row) * p.k + static_cast<size_t>(sb0 + b) * kQK) + 2 * lane;
-        const float4 lo = __ldg(src), hi = __ldg(src + 1);
+        const float4 lo = load_f4(src), hi = load_f4(src + 1);
         v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
         v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
     };
@@ -634,7 +641,7 @@ q4k_moe_gemv_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             for (int i = threadIdx.x; i < r.count * p.cap * kVRows; i += kVThreads) {
                 const int unit = i / (p.cap * kVRows), v = i / kVRows % p.cap, row = i % kVRows;
                 if (unit % csize != rank || v >= vecs || !sound) continue;
-                const int pair = __ldg(p.g.order + slot0 + v);
+                const int pair = p.g.order[slot0 + v];
                 // the warps whose items touch the unit
                 const int wa = ((unit * cols + 1) * kVWarps - 1) / items, wb = ((unit + 1) * cols * kVWarps - 1) / items;
                 double sum[2] = {0.0, 0.0};

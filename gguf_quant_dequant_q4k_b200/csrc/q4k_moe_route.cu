@@ -57,7 +57,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Token t's choices and weights, by one warp. S: keys per lane, experts <= 32 S.
 template <int S>
-__device__ __forceinline__ void choose_token(const float* __restrict__ logits, int* __restrict__ ids,
+__device__ __forceinline__ void choose_token(const float* logits, int* __restrict__ ids,
                                              float* __restrict__ weights, long long t, int n_experts, int top_k,
                                              bool renorm, int lane) {
     const float* row = logits + t * n_experts;
@@ -65,7 +65,7 @@ __device__ __forceinline__ void choose_token(const float* __restrict__ logits, i
 #pragma unroll
     for (int i = 0; i < S; ++i) {
         const int e = 32 * i + lane;
-        key[i] = e < n_experts ? logit_key(__ldg(row + e)) : 0u;
+        key[i] = e < n_experts ? logit_key(row[e]) : 0u;
     }
     float top = 0.f, all = 0.f, mine = 0.f;   // lane j keeps the j-th choice
     int chosen = -1;
@@ -208,7 +208,7 @@ __device__ __forceinline__ void group_pairs(GroupShared& sh, const int* ids, int
 
 template <int S>
 __global__ void __launch_bounds__(kChooseThreads)
-q4k_moe_choose_kernel(const float* __restrict__ logits, int* __restrict__ ids, float* __restrict__ weights,
+q4k_moe_choose_kernel(const float* logits, int* __restrict__ ids, float* __restrict__ weights,
                       int n_tokens, int n_experts, int top_k, bool renorm) {
     pdl_launch_dependents();
     pdl_wait();
@@ -229,7 +229,7 @@ q4k_moe_group_kernel(const int* ids, int* __restrict__ offsets, int* __restrict_
 
 template <int S>
 __global__ void __launch_bounds__(kGroupThreads)
-q4k_moe_route_small_kernel(const float* __restrict__ logits, int* ids, float* __restrict__ weights,
+q4k_moe_route_small_kernel(const float* logits, int* ids, float* __restrict__ weights,
                            int* __restrict__ offsets, int* __restrict__ order, int n_tokens, int n_experts, int top_k,
                            bool renorm) {
     __shared__ GroupShared sh;
