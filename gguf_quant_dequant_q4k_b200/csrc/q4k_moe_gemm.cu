@@ -48,7 +48,6 @@
 #include "q4k_moe.h"
 #include "q4k_pair.cuh"
 #include "q4k_superblock.cuh"
-#include "q4k_swiglu.cuh"
 
 namespace q4k {
 
@@ -162,6 +161,14 @@ struct TileWalk {
     }
     __device__ __forceinline__ void next() { tile += static_cast<int>(gridDim.x >> 1); }
 };
+
+// silu(g) * u for a result that is rounded to fp16 (silu_mul, q4k_swiglu.cuh, is
+// the f32 form): __expf is off by at most 2 + 1.173 |g| ulp and __fdividef by 2,
+// together under 2^-16 relative for |g| <= 88 against fp16's half step of 2^-11;
+// below -88 the exponential overflows and the quotient is 0.
+__device__ __forceinline__ float silu_mul_fast(float g, float u) {
+    return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float2 v) {
     const __half2 h = __floats2half2_rn(v.x, v.y);

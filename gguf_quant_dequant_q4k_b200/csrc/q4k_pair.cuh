@@ -1,7 +1,7 @@
 // q4k_pair.cuh -- sm_100a primitives of a CTA pair (a cluster of two CTAs whose
 // tensor cores work on one tile): remote mbarrier arrivals, tensor-core
-// instructions of cta_group::2, TMA loads that signal the pair's first CTA, and
-// register reallocation between warp roles. No TMA multicast.
+// instructions of cta_group::2, TMA loads that signal the pair's first CTA, TMEM
+// loads, and register reallocation between warp roles. No TMA multicast.
 #pragma once
 
 #include <cstdint>
@@ -96,6 +96,19 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// 16 consecutive TMEM columns of the calling thread's lane (valid after
+// tmem_wait_ld()).
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 

@@ -12,12 +12,4 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
 }
 
-// The same for a result that is rounded to fp16: __expf is off by at most
-// 2 + 1.173 |g| ulp and __fdividef by 2, together under 2^-16 relative for
-// |g| <= 88 against fp16's half step of 2^-11; below -88 the exponential
-// overflows and the quotient is 0.
-__device__ __forceinline__ float silu_mul_fast(float g, float u) {
-    return __fdividef(g, 1.0f + __expf(-g)) * u;
-}
-
 }  // namespace q4k
