@@ -104,3 +104,95 @@ def test_experts_with_sound_offsets_survive_bad_ones(q4k, per_row, mats, half, b
         assert (np.abs(y[rows] - want) <= tol).all(), f"expert {e}"
         skipped[rows] = False
     assert (y[skipped] == base.FILL).all()
+
+
+# The 64-bit product on the device: every output of cases that are too large for the CPU oracle's loops.
+
+def reference64(q4k, p):
+    """(values, sums of magnitudes) per slot and matrix, float64 on the device, of the
+    weights that q4k_dequant_f16 gives (test_gpu_prefill.py: the oracle's bits)."""
+    rows = torch.from_numpy(np.ascontiguousarray(base.ref.x_row(p.order, p.per_row))).cuda()
+    x = p.dx.double()
+    out = []
+    mirror = torch.empty((p.n, p.k), dtype=torch.float16, device="cuda")
+    for w in p.dw:
+        y, a = (torch.zeros((p.pairs, p.n), dtype=torch.float64, device="cuda") for _ in range(2))
+        for e in range(p.experts):
+            s0, s1 = int(p.offsets[e]), int(p.offsets[e + 1])
+            if s0 == s1:
+                continue
+            q4k.q4k_dequant_f16(w[e].contiguous(), mirror, p.n, p.k)
+            m = mirror.double()
+            xe = x[rows[s0:s1]]
+            y[s0:s1], a[s0:s1] = xe @ m.T, xe.abs() @ m.abs().T
+        out.append((y, a))
+    return out
+
+
+def plain_tolerance(a, k):
+    """q4k_moe_gemm_f16: the q4k_gemm_f16 bound of sums of at most 768 products
+    (768 * 2^-23 sum|w x|, 1e-6), then one f32 addition, rounded to nearest, for each
+    such sum (2^-24 of a partial sum, itself at most 1.0001 sum|w x|)."""
+    return (min(k, 768) * 2.0 ** -23 + 1.0001 * -(-k // 768) * 2.0 ** -24) * a + 1e-6
+
+
+def check64(q4k, p, y, what):
+    got = y.double()
+    live = int(p.offsets[-1])
+    ref64 = reference64(q4k, p)
+    if len(p.ws) == 1:
+        (want, a), = ref64
+        tol = plain_tolerance(a, p.k)
+        got = got[torch.from_numpy(p.order[:live].astype(np.int64)).cuda()]
+    else:
+        (g, ag), (u, au) = ref64
+        tg, tu = (p.k * 2.0 ** -23 * a + 1e-6 for a in (ag, au))
+        s = g * torch.sigmoid(g)
+        want = s * u
+        tol = 1.1 * tg * (u.abs() + tu) + (s.abs() + 1.1 * tg) * tu + 1e-6 * want.abs() + 1e-30
+        tol = tol + 2.0 ** -11 * (want.abs() + tol) + 2.0 ** -25      # the rounding to binary16
+        got = got[:live]
+    err = (got - want[:live]).abs()
+    bad = ~(err <= tol[:live])
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} out of tolerance"
+
+
+MANY_TILES = [  # pairs per expert, rows of the plain and of the gate/up form, k: two or more tiles per pair of CTAs
+    ([700, 13, 0, 487], 7300, 3700, 1280),                                 # large groups, blocks of up to 192 / 256 slots
+    ([1025], 10100, 5000, 1024),                                           # one expert
+    ([500, 130, 1, 0, 64, 33] + [20] * 10, 4900, 2500, 1280),              # small groups, one of them in four blocks
+]
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("counts,n_plain,n_gated,k", MANY_TILES)
+def test_gemm_many_tiles_per_pair(q4k, counts, n_plain, n_gated, k, mats):
+    """Every pair of CTAs takes several tiles of several superblocks: accumulators,
+    rings and decoded weights are reused across tiles. Every output is compared."""
+    ids = np.random.default_rng(6).permutation(np.repeat(np.arange(len(counts)), counts)).astype(np.int32).reshape(-1, 1)
+    n = n_plain if mats == 1 else n_gated
+    slots = (192 if mats == 1 else 256) if len(ids) > 96 * len(counts) else 128
+    tiles = sum(-(-c // slots) for c in counts) * -(-n // (256 if mats == 1 else 128))
+    assert tiles > 2 * 74
+    p = base.Problem(len(ids), len(counts), 1, n, k, 300 + n, mats=mats, half=True, ids=ids)
+    y = base.run_product(q4k, p)
+    check64(q4k, p, y, f"{len(ids)} pairs {len(counts)}x{n}x{k}")
+    assert torch.equal(base.run_product(q4k, p), y)
+    assert q4k.q4k_device_fault_flags() == 0
+
+
+def test_gemm_long_sums_of_one_sign(q4k):
+    """Sums of positive terms, where an accumulator that cuts off instead of rounding
+    drifts one way, over rows of 1024 superblocks: the plain form keeps the bound of
+    sums of 768 products."""
+    n, k, experts, tokens = 24, 262144, 2, 5
+    rng = np.random.default_rng(8)
+    some = np.stack([base.oracle.pack(0x0C00, 0, rng.integers(8, 64, 8), np.zeros(8, int), rng.integers(1, 16, 256))
+                     for _ in range(64)])                                  # d = 2^-12, no minimum
+    p = base.Problem(tokens, experts, 1, n, 256, 24, half=True)
+    p.k = k
+    p.ws = [some[rng.integers(0, 64, experts * n * (k // 256))].reshape(experts, -1)]
+    p.dw = [base.dev(p.ws[0])]
+    p.x = rng.uniform(0.5, 1.0, (tokens, k)).astype(np.float16).view(np.uint16)
+    p.dx = base.dev(p.x).view(torch.float16)
+    check64(q4k, p, base.run_product(q4k, p), "long sums")
