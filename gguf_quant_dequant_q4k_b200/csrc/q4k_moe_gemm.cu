@@ -42,11 +42,11 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_fp16.h>
-#include <mutex>
 
 #include "q4k_internal.h"
 #include "q4k_moe.h"
 #include "q4k_pair.cuh"
+#include "q4k_per_device.h"
 #include "q4k_superblock.cuh"
 
 namespace q4k {
@@ -695,32 +695,32 @@ bool make_moe_x_map(CUtensorMap* map, const void* x, int rows, int k, int box_ro
 constexpr uint64_t kPoolKeepBytes = 512ull << 20;
 
 cudaError_t workspace_pool(cudaMemPool_t* pool) {
-    constexpr int kDevices = 64;
-    static std::once_flag once[kDevices];
-    static cudaMemPool_t pools[kDevices];
-    static cudaError_t status[kDevices];
+    static PerDevice<cudaMemPool_t> pools;
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
-    std::call_once(once[dev], [dev] {
+    return pools.get(dev, pool, [dev](cudaMemPool_t* made) {
         // the first call may be inside a capture, which a pool's creation would end in the default mode
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-        status[dev] = cudaThreadExchangeStreamCaptureMode(&mode);
-        if (status[dev] != cudaSuccess) return;
+        cudaError_t status = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (status != cudaSuccess) return status;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
-        status[dev] = cudaMemPoolCreate(&pools[dev], &props);
-        uint64_t keep = kPoolKeepBytes;
-        if (status[dev] == cudaSuccess)
-            status[dev] = cudaMemPoolSetAttribute(pools[dev], cudaMemPoolAttrReleaseThreshold, &keep);
+        status = cudaMemPoolCreate(made, &props);
+        if (status == cudaSuccess) {
+            uint64_t keep = kPoolKeepBytes;
+            status = cudaMemPoolSetAttribute(*made, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (status != cudaSuccess) cudaMemPoolDestroy(*made);
+        }
         const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
-        if (status[dev] == cudaSuccess) status[dev] = back;
+        if (status == cudaSuccess && back != cudaSuccess) {
+            cudaMemPoolDestroy(*made);
+            status = back;
+        }
+        return status;
     });
-    *pool = pools[dev];
-    return status[dev];
 }
 
 }  // namespace

@@ -39,13 +39,13 @@
 //   vectors per group the issue slots set the pace.
 #include <cstdint>
 #include <cuda.h>
-#include <mutex>
 #include <type_traits>
 
 #include "q4k_internal.h"
 #include "q4k_moe.cuh"
 #include "q4k_moe.h"
 #include "q4k_pair.cuh"
+#include "q4k_per_device.h"
 #include "q4k_superblock.cuh"
 #include "q4k_swiglu.cuh"
 
@@ -699,14 +699,18 @@ bool make_gemv_map(CUtensorMap* map, const void* w, long long rows, int nsb) {
 // Clusters of csize CTAs that the current device holds at once: a cluster lies
 // in one GPC, so several SMs may stay without one, and a cluster more than fits
 // would run after all others.
-int gemv_clusters(int csize, int num_sms) {
-    if (csize == 1) return num_sms;
-    constexpr int kDevices = 64;
-    static std::once_flag once[kDevices];
-    static int fit[kDevices][4];
+cudaError_t gemv_clusters(int csize, int num_sms, int* clusters) {
+    *clusters = num_sms;
+    if (csize == 1) return cudaSuccess;
+    struct Fit {
+        int of[4];   // by the logarithm of the size
+    };
+    static PerDevice<Fit> fits;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
-    std::call_once(once[dev], [dev] {
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Fit fit;
+    e = fits.get(dev, &fit, [](Fit* made) {
         for (int i = 1; i <= 3; ++i) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(1u << i);
@@ -719,11 +723,15 @@ int gemv_clusters(int csize, int num_sms) {
             attr[0].val.clusterDim.z = 1;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&fit[dev][i], q4k_moe_gemv_kernel<true>, &cfg) != cudaSuccess) fit[dev][i] = 0;
+            const cudaError_t query = cudaOccupancyMaxActiveClusters(&made->of[i], q4k_moe_gemv_kernel<true>, &cfg);
+            if (query != cudaSuccess) return query;
         }
+        return cudaSuccess;
     });
-    const int got = fit[dev][csize == 2 ? 1 : csize == 4 ? 2 : 3];
-    return got < num_sms / csize ? got : num_sms / csize;
+    if (e != cudaSuccess) return e;
+    const int got = fit.of[csize == 2 ? 1 : csize == 4 ? 2 : 3];
+    *clusters = got < num_sms / csize ? got : num_sms / csize;
+    return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -742,8 +750,9 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     int csize = 1, cap = g.pairs <= g.experts ? 2 : kVMaxVec;
     while (csize < kVMaxCluster && (nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) csize *= 2;
     if ((nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) cap = 2;
-    const int clusters = gemv_clusters(csize, dev.sm_count);
-    if (clusters <= 0) return cuda_failure(cudaErrorInvalidConfiguration);
+    int clusters = 0;
+    cudaError_t e = gemv_clusters(csize, dev.sm_count, &clusters);
+    if (e != cudaSuccess) return cuda_failure(e);
     MoeGemvParams p{};
     p.g = g;
     p.x = x;
@@ -768,8 +777,8 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<true>, mw, mw2, p)
-                                 : cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<false>, mw, mw2, p);
+    e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<true>, mw, mw2, p)
+               : cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<false>, mw, mw2, p);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 
