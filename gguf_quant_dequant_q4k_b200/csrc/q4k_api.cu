@@ -77,10 +77,6 @@ int current_device_info(DeviceInfo* info) {
             g_dev_status[dev] = q4k_last_cuda_error_value();
         if (g_dev_status[dev] == 0 && i8_set_attributes() != Q4K_OK)
             g_dev_status[dev] = q4k_last_cuda_error_value();
-        if (g_dev_status[dev] == 0 && moe_gemv_set_attributes() != Q4K_OK)
-            g_dev_status[dev] = q4k_last_cuda_error_value();
-        if (g_dev_status[dev] == 0 && moe_gemm_set_attributes() != Q4K_OK)
-            g_dev_status[dev] = q4k_last_cuda_error_value();
         if (g_dev_status[dev] == 0) {
             stream_cluster_occupancy(1, g_dev[dev].max_clusters[0]);
             stream_cluster_occupancy(2, g_dev[dev].max_clusters[1]);

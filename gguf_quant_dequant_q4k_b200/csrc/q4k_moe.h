@@ -38,8 +38,6 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
 int launch_moe_combine(const float* z, const int* ids, const float* weights, const float* residual, float* y,
                        int n_tokens, int top_k, int hidden, int num_sms, cudaStream_t stream);
 
-int moe_gemv_set_attributes();
-int moe_gemm_set_attributes();
 int read_moe_gemv_fault_flags(unsigned* flags);
 int read_moe_gemm_fault_flags(unsigned* flags);
 

@@ -723,6 +723,28 @@ cudaError_t workspace_pool(cudaMemPool_t* pool) {
     });
 }
 
+// The kernels' attributes, set by the device's first call (not with the library's
+// other kernels, so that programs without experts load none of this).
+cudaError_t gemm_ready() {
+    static PerDevice<bool> ready;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    bool set;
+    return ready.get(dev, &set, [](bool* made) {
+        constexpr cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaError_t status = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, true>, smem, MoeShape<true, true>::smem);
+        if (status == cudaSuccess)
+            status = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, false>, smem, MoeShape<true, false>::smem);
+        if (status == cudaSuccess)
+            status = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, true>, smem, MoeShape<false, true>::smem);
+        if (status == cudaSuccess)
+            status = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, false>, smem, MoeShape<false, false>::smem);
+        *made = true;
+        return status;
+    });
+}
+
 }  // namespace
 
 int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const void* x_f16, const MoeGroups& g, void* y,
@@ -731,6 +753,8 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
     const int nsb = k / kQK;
     const long long rows = static_cast<long long>(g.experts) * n;
     if (encode_tiled() == nullptr) return cuda_failure(cudaErrorInvalidValue);
+    cudaError_t e = gemm_ready();
+    if (e != cudaSuccess) return cuda_failure(e);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -741,7 +765,6 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
 
     const void* xs = x_f16;      // rows in slot order
     void* work = nullptr;
-    cudaError_t e = cudaSuccess;
     if (g.per_row > 0) {
         cudaMemPool_t pool = nullptr;
         e = workspace_pool(&pool);
@@ -782,15 +805,6 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
         const cudaError_t f = cudaFreeAsync(work, stream);
         if (e == cudaSuccess) e = f;
     }
-    return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
-}
-
-int moe_gemm_set_attributes() {
-    constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, true>, attr, MoeShape<true, true>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<true, false>, attr, MoeShape<true, false>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, true>, attr, MoeShape<false, true>::smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemm_kernel<false, false>, attr, MoeShape<false, false>::smem);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 

@@ -698,10 +698,9 @@ bool make_gemv_map(CUtensorMap* map, const void* w, long long rows, int nsb) {
 
 // Clusters of csize CTAs that the current device holds at once: a cluster lies
 // in one GPC, so several SMs may stay without one, and a cluster more than fits
-// would run after all others.
+// would run after all others. The device's first call also sets the kernels'
+// attributes (here, so that programs without experts load none of this).
 cudaError_t gemv_clusters(int csize, int num_sms, int* clusters) {
-    *clusters = num_sms;
-    if (csize == 1) return cudaSuccess;
     struct Fit {
         int of[4];   // by the logarithm of the size
     };
@@ -711,6 +710,10 @@ cudaError_t gemv_clusters(int csize, int num_sms, int* clusters) {
     if (e != cudaSuccess) return e;
     Fit fit;
     e = fits.get(dev, &fit, [](Fit* made) {
+        constexpr cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        cudaError_t set = cudaFuncSetAttribute(q4k_moe_gemv_kernel<true>, smem, kVSmemLimit);
+        if (set == cudaSuccess) set = cudaFuncSetAttribute(q4k_moe_gemv_kernel<false>, smem, kVSmemLimit);
+        if (set != cudaSuccess) return set;
         for (int i = 1; i <= 3; ++i) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(1u << i);
@@ -729,6 +732,8 @@ cudaError_t gemv_clusters(int csize, int num_sms, int* clusters) {
         return cudaSuccess;
     });
     if (e != cudaSuccess) return e;
+    *clusters = num_sms;
+    if (csize == 1) return cudaSuccess;
     const int got = fit.of[csize == 2 ? 1 : csize == 4 ? 2 : 3];
     *clusters = got < num_sms / csize ? got : num_sms / csize;
     return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
@@ -779,13 +784,6 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     cfg.numAttrs = 2;
     e = swiglu ? cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<true>, mw, mw2, p)
                : cudaLaunchKernelEx(&cfg, q4k_moe_gemv_kernel<false>, mw, mw2, p);
-    return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
-}
-
-int moe_gemv_set_attributes() {
-    constexpr cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t e = cudaFuncSetAttribute(q4k_moe_gemv_kernel<true>, attr, kVSmemLimit);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(q4k_moe_gemv_kernel<false>, attr, kVSmemLimit);
     return e == cudaSuccess ? Q4K_OK : cuda_failure(e);
 }
 

@@ -30,3 +30,13 @@ def test_failed_attempts_are_tried_again(tmp_path):
 def test_no_first_status_is_kept(path):
     with open(path) as f:
         assert "once_flag" not in f.read()
+
+
+def test_dense_calls_load_no_expert_kernels():
+    """The set-up of every call's device info touches the dense kernels only: a
+    program without experts neither waits for the others to load nor fails with them."""
+    with open(os.path.join(CSRC, "q4k_api.cu")) as f:
+        text = f.read()
+    start = text.index("int current_device_info(")
+    body = text[start:text.index("}  // namespace q4k", start)]
+    assert "set_attributes" in body and "moe" not in body
