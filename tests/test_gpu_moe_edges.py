@@ -196,3 +196,30 @@ def test_gemm_long_sums_of_one_sign(q4k):
     p.x = rng.uniform(0.5, 1.0, (tokens, k)).astype(np.float16).view(np.uint16)
     p.dx = base.dev(p.x).view(torch.float16)
     check64(q4k, p, base.run_product(q4k, p), "long sums")
+
+
+# ------------------------------------------------------------------ combination
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("top_k", range(1, 17))
+def test_combine_every_top_k(q4k, top_k, residual):
+    """Tokens with all, some and no choices; rows of z without an expert hold NaN and
+    are not read."""
+    t, hidden = 37, 132
+    rng = np.random.default_rng(top_k)
+    ids = rng.integers(-1, 6, (t, top_k)).astype(np.int32)
+    ids[0], ids[1] = -1, 0
+    z = rng.standard_normal((t, top_k, hidden)).astype(np.float32)
+    z[ids < 0] = np.nan
+    w = rng.random((t, top_k)).astype(np.float32)
+    res = rng.standard_normal((t, hidden)).astype(np.float32)
+    y = torch.full((t, hidden), base.FILL, device="cuda")
+    q4k.q4k_moe_combine(base.dev(z), base.dev(ids), base.dev(w), base.dev(res) if residual else None, y, t, top_k, hidden)
+    live = (ids >= 0)[..., None]
+    terms = np.where(live, z, 0).astype(np.float64) * np.where(live, w[..., None], 0)
+    start = res.astype(np.float64) if residual else np.zeros((t, hidden))
+    # each fma rounds once: half a step, 2^-24, of a partial sum of at most the sum of magnitudes
+    tol = top_k * 2.0 ** -24 * 1.0001 * (np.abs(start) + np.abs(terms).sum(1)) + 1e-37
+    err = np.abs(y.cpu().numpy().astype(np.float64) - (start + terms.sum(1)))
+    assert (err <= tol).all(), f"worst {np.nanmax(err / tol):.3g}"
+    assert np.array_equal(y[0].cpu().numpy(), start[0].astype(np.float32))
