@@ -2,9 +2,8 @@
 // each token's top_k experts and their softmax weights, and the pairs (token,
 // choice) grouped by expert.
 //
-// No workspace; the lists do not depend on timing. Small batches
-// (up to kSmallTokens): one CTA does both steps in one launch. Others: two
-// launches.
+// No workspace; the lists do not depend on timing. Small batches (one_launch): one
+// CTA does both steps in one launch. Others: two launches.
 // * choose: a warp per token. A lane holds experts lane, lane + 32, ... as
 //   order-preserving integer keys; each of the top_k rounds takes the warp's
 //   maximum (redux) and, among equal keys, the lowest expert. The weights are
@@ -36,6 +35,18 @@ constexpr int kGroupCtas = 8;        // portable cluster size
 constexpr int kGroupBatch = 8;       // ids per lane in flight
 constexpr int kSmallTokens = 64;     // two tokens per warp of the one CTA
 static_assert(kSmallTokens * Q4K_MOE_MAX_TOP_K <= 1024, "one pass of 32 pairs per warp");
+
+// One launch or two. A warp's second token costs as much again, the more the more
+// rounds (top_k) and keys per lane (s). Measured, one launch against two, us:
+//   8 experts, top 2:    16 tokens 3.0 / 4.7    32: 3.3 / 4.7     64: 4.3 / 4.7
+//   8 experts, top 4:                           33: 4.7 / 5.0     64: 5.2 / 5.1
+//   64 experts, top 2:                          33: 4.7 / 5.2     64: 5.2 / 5.2
+//   64 experts, top 8:   16: 4.5 / 5.9          32: 5.6 / 6.2     64: 8.4 / 6.4
+//   128 experts, top 2:                         33: 5.5 / 5.7     64: 6.1 / 5.7
+//   256 experts, top 16: 16: 9.0 / 9.2          32: 12.8 / 9.5    64: 23.1 / 10.6
+bool one_launch(int n_tokens, int top_k, int s) {
+    return n_tokens <= 32 || (n_tokens <= kSmallTokens && top_k + s <= 5);
+}
 
 // Larger float, larger key; equal floats, equal keys (-0.0 + 0.0 is +0.0); NaN
 // and -inf get 0 (never chosen), +inf the key of FLT_MAX.
@@ -259,7 +270,7 @@ cudaError_t launch_route(const RouteArgs& a, int num_sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (a.n_tokens <= kSmallTokens) {
+    if (one_launch(a.n_tokens, a.top_k, S)) {
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kGroupThreads);
         return cudaLaunchKernelEx(&cfg, q4k_moe_route_small_kernel<S>, a.logits, a.ids, a.weights, a.offsets, a.order,

@@ -18,7 +18,7 @@ q4k = base.q4k     # the module's fixture
                                        (64, 100, 16), (200, 256, 16)])
 def test_route_signed_zeros_tie(q4k, t, e, top_k, renorm):
     """-0.0 and +0.0 are equal logits: the lower expert comes first, in the one-launch
-    (up to 64 tokens) and the two-launch path, wherever the tie lies."""
+    (small batches) and the two-launch path, wherever the tie lies."""
     rng = np.random.default_rng(t * 100 + e)
     zeros = np.where(rng.random((t, e)) < 0.5, np.float32(-0.0), np.float32(0.0))
     logits = np.where(rng.random((t, e)) < 0.7, zeros, rng.choice(np.float32([-1, 1, 2]), (t, e)))
@@ -28,6 +28,14 @@ def test_route_signed_zeros_tie(q4k, t, e, top_k, renorm):
     logits = logits.astype(np.float32)
     assert np.signbit(logits[0, 0])
     base.check_route(base.gpu_route(q4k, logits, top_k, renorm), logits, top_k, renorm, f"{t}x{e} top {top_k}")
+
+
+@pytest.mark.parametrize("t", [31, 32, 33])
+@pytest.mark.parametrize("e,top_k", [(8, 2), (64, 8), (256, 16)])
+def test_route_around_the_one_launch_limit(q4k, t, e, top_k):
+    logits = np.random.default_rng(t + e).standard_normal((t, e)).astype(np.float32)
+    logits[3] = -np.inf
+    base.check_route(base.gpu_route(q4k, logits, top_k, True), logits, top_k, True, f"{t}x{e} top {top_k}")
 
 
 def test_route_of_the_most_tokens(q4k):
