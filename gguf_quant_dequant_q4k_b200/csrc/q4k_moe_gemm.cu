@@ -102,10 +102,16 @@ struct MoeShape {
     static_assert(b_stages >= a_steps, "a step's barrier is reused behind its A buffers");
     static_assert(smem <= 227 * 1024 - 4096, "shared memory");
 };
-// At most this many pairs per expert on average: narrow. (Measured at 512 pairs per
-// expert: wide 743 us against narrow 1000, gate/up; with about 48 the blocks are the
-// same, and narrow keeps two accumulators and eight stages.)
-constexpr int kNarrowPairsPerExpert = 96;
+// At most this many pairs per expert on average: narrow. Measured, narrow against wide, us, for 64 / 96 / 128 / 192 /
+// 256 / 384 pairs per expert (a router that prefers some experts; the groups differ by a factor of about four):
+//   gate/up, 64 experts 1536 x 2048:  108/116, 132/133, 157/153, 207/195, 261/238, 367/328
+//   gate/up, 8 experts 14336 x 4096:  214/222, 264/260, 328/287, 425/371, 536/459, 741/617
+//   plain, 64 experts 2048 x 1536:    61/76, 71/86, 84/99, 110/118, 139/147, 191/199
+//   plain, 8 experts 4096 x 14336:    117/125, 140/152, 168/166, 222/219, 281/285, 395/380
+// In the plain form the narrow shape fills its second accumulator while the first is drained, which the wide one waits
+// for; beyond 128 pairs, where wide has one block and narrow two, it depends on the tiles' number (6 experts 2048 x 4096,
+// 160 pairs: 36/29; 4 experts 3900 x 9984: 75/97). The average decides: an expert far above it runs in blocks of 128.
+constexpr int kNarrowPairsGated = 96, kNarrowPairsPlain = 128;
 
 struct MoeShared {
     uint64_t w_full[kMaxWStages], w_empty[kMaxWStages];
@@ -792,7 +798,7 @@ int launch_moe_gemm(const DeviceInfo& dev, const void* w, const void* w2, const 
         p.nsb = nsb;
         const int tile_rows = swiglu ? kCtaRows : 2 * kCtaRows;
         p.row_tiles = (n + tile_rows - 1) / tile_rows;
-        const bool wide = g.pairs > static_cast<long long>(kNarrowPairsPerExpert) * g.experts;
+        const bool wide = g.pairs > static_cast<long long>(swiglu ? kNarrowPairsGated : kNarrowPairsPlain) * g.experts;
         cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count / 2 * 2));
         cfg.blockDim = dim3(MoeShape<true, true>::threads);
         cfg.dynamicSmemBytes = swiglu ? (wide ? MoeShape<true, true>::smem : MoeShape<true, false>::smem)

@@ -172,6 +172,17 @@ MANY_TILES = [  # pairs per expert, rows of the plain and of the gate/up form, k
 ]
 
 
+@pytest.mark.parametrize("counts", [[96], [97], [128], [129], [192], [193], [256], [257], [384], [385], [513], [500, 14], [0, 514]])
+@pytest.mark.parametrize("mats", [1, 2])
+def test_gemm_block_limits(q4k, counts, mats):
+    """Numbers of pairs around the limits of the shapes and of their blocks."""
+    ids = np.random.default_rng(7).permutation(np.repeat(np.arange(len(counts)), counts)).astype(np.int32).reshape(-1, 1)
+    p = base.Problem(len(ids), len(counts), 1, 290, 1280, 310 + len(ids), mats=mats, half=True, ids=ids)
+    y = base.run_product(q4k, p)
+    check64(q4k, p, y, f"{counts}")
+    assert torch.equal(base.run_product(q4k, p), y)
+
+
 @pytest.mark.parametrize("mats", [1, 2])
 @pytest.mark.parametrize("counts,n_plain,n_gated,k", MANY_TILES)
 def test_gemm_many_tiles_per_pair(q4k, counts, n_plain, n_gated, k, mats):
@@ -179,7 +190,7 @@ def test_gemm_many_tiles_per_pair(q4k, counts, n_plain, n_gated, k, mats):
     rings and decoded weights are reused across tiles. Every output is compared."""
     ids = np.random.default_rng(6).permutation(np.repeat(np.arange(len(counts)), counts)).astype(np.int32).reshape(-1, 1)
     n = n_plain if mats == 1 else n_gated
-    slots = (192 if mats == 1 else 256) if len(ids) > 96 * len(counts) else 128
+    slots = (192 if mats == 1 else 256) if len(ids) > (128 if mats == 1 else 96) * len(counts) else 128
     tiles = sum(-(-c // slots) for c in counts) * -(-n // (256 if mats == 1 else 128))
     assert tiles > 2 * 74
     p = base.Problem(len(ids), len(counts), 1, n, k, 300 + n, mats=mats, half=True, ids=ids)
