@@ -113,13 +113,13 @@ struct GemvShared {   // static: below the 6 KB that kVSmemLimit leaves
     int abort;
 };
 
+static_assert(sizeof(GemvShared) <= 6144 - 256, "shared memory");
+
 // What a unit of an expert's groups costs: three or four vectors are two columns
 // of MMAs.
 __device__ __forceinline__ int unit_cost(int cnt, int chunks) { return cnt > 2 * chunks ? kCost4 : kCost2; }
 
 // d = A B^T: A 16 x 32 unsigned bytes (a0, a2: row g, a1, a3: row g + 8), B 8 x 32 signed.
-static_assert(sizeof(GemvShared) <= 6144 - 256, "shared memory");
-
 __device__ __forceinline__ void imma(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                      uint32_t b1) {
     asm volatile(
