@@ -242,3 +242,177 @@ def test_combine_every_top_k(q4k, top_k, residual):
     err = np.abs(y.cpu().numpy().astype(np.float64) - (start + terms.sum(1)))
     assert (err <= tol).all(), f"worst {np.nanmax(err / tol):.3g}"
     assert np.array_equal(y[0].cpu().numpy(), start[0].astype(np.float32))
+
+
+# ------------------------------------------------------------------ large buffers, graphs, threads
+
+def device_weights(experts, n, k, seed):
+    """Random superblocks made on the device: d = 2^-12, dmin = 2^-9, other bytes at random."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    w = torch.randint(0, 256, (experts, n * (k // 256), 144), dtype=torch.uint8, device="cuda", generator=gen)
+    w[..., 0:4] = torch.tensor([0x00, 0x0C, 0x00, 0x18], dtype=torch.uint8, device="cuda")
+    return w
+
+
+@pytest.mark.parametrize("name", ["gemv", "gemv_swiglu", "gemm", "gemm_swiglu"])
+def test_weights_beyond_4_gib(q4k, name):
+    """Experts whose matrices lie behind 2^32 bytes of the operand."""
+    experts, n, k = 160, 14336, 4096
+    if torch.cuda.mem_get_info()[0] < 16e9:
+        pytest.skip("needs 16 GB of device memory")
+    half, gated = name.startswith("gemm"), name.endswith("swiglu")
+    w = device_weights(experts, n, k, 1)
+    assert w.numel() > 2 ** 32 and (experts - 1) * n * (k // 256) * 144 > 2 ** 32
+    ids = np.array([159, 0, 158, 159, 127, 159], np.int32).reshape(-1, 1)     # 127: across 2^32
+    off, order = base.ref.group(ids, experts)
+    x = torch.randn(6, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) / 64
+    x = x.half() if half else x
+    y = torch.full((6, n), base.FILL, device="cuda", dtype=torch.float16 if half and gated else torch.float32)
+    fn = getattr(q4k, "q4k_moe_" + name + ("_f16" if half else ""))
+    fn(*([w, w] if gated else [w]), x, base.dev(off), base.dev(order), y, experts, 6, 1, n, k)
+    m16 = torch.empty((n, k), dtype=torch.float16, device="cuda")
+    m32 = torch.empty((n, k), device="cuda")
+    for slot, pair in enumerate(order):
+        e = int(ids[pair, 0])
+        if half:
+            q4k.q4k_dequant_f16(w[e], m16, n, k)
+        else:
+            q4k.q4k_dequant_f32(w[e], m32, n, k)
+        m, xr = (m16 if half else m32).double(), x[int(pair)].double()
+        v, a = m @ xr, m.abs() @ xr.abs()
+        tol = plain_tolerance(a, k) if half and not gated else k * 2.0 ** -23 * a + 1e-6 if half else 1e-4 * a + 1e-6
+        if gated:
+            s = v * torch.sigmoid(v)
+            tol = 1.1 * tol * (v.abs() + tol) + (s.abs() + 1.1 * tol) * tol + 1e-6 * (s * v).abs() + 1e-30
+            v = s * v
+            if half:
+                tol = tol + 2.0 ** -11 * (v.abs() + tol) + 2.0 ** -25
+        got = y[slot if gated else int(pair)].double()
+        assert bool(((got - v).abs() <= tol).all()), f"expert {e}"
+    assert q4k.q4k_device_fault_flags() == 0
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+def test_outputs_beyond_2_31_elements(q4k, mats):
+    """More than 2^31 outputs: rows at the start, around 2^31 elements and at the end."""
+    pairs, n, k = 70001, 31000, 256
+    if torch.cuda.mem_get_info()[0] < 16e9:
+        pytest.skip("needs 16 GB of device memory")
+    assert pairs * n > 2 ** 31
+    ids = (np.arange(pairs, dtype=np.int32) % 2).reshape(-1, 1)
+    off, order = base.ref.group(ids, 2)
+    ws = [device_weights(2, n, k, 3 + i) for i in range(mats)]
+    x = (torch.randn(pairs, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(4)) / 8).half()
+    y = torch.full((pairs, n), base.FILL, device="cuda", dtype=torch.float16 if mats == 2 else torch.float32)
+    fn = q4k.q4k_moe_gemm_swiglu_f16 if mats == 2 else q4k.q4k_moe_gemm_f16
+    fn(*ws, x, base.dev(off), base.dev(order), y, 2, pairs, 1, n, k)
+    mirror = torch.empty((n, k), dtype=torch.float16, device="cuda")
+    at = 2 ** 31 // n
+    for row in (0, 1, at - 1, at, at + 1, pairs - 2, pairs - 1):
+        pair = int(order[row]) if mats == 2 else row
+        xr, vs, ts = x[pair].double(), [], []
+        for w in ws:
+            q4k.q4k_dequant_f16(w[pair % 2], mirror, n, k)
+            m = mirror.double()
+            vs.append(m @ xr)
+            ts.append(plain_tolerance(m.abs() @ xr.abs(), k))
+        v, tol = vs[0], ts[0]
+        if mats == 2:
+            s = v * torch.sigmoid(v)
+            tol = 1.1 * ts[0] * (vs[1].abs() + ts[1]) + (s.abs() + 1.1 * ts[0]) * ts[1] + 1e-6 * (s * vs[1]).abs() + 1e-30
+            v = s * vs[1]
+            tol = tol + 2.0 ** -11 * (v.abs() + tol) + 2.0 ** -25
+        assert bool(((y[row].double() - v).abs() <= tol).all()), f"row {row}"
+    assert bool((y[:, 0] != base.FILL).all()) and bool((y[:, n - 1] != base.FILL).all())
+    del x, y
+    torch.cuda.empty_cache()
+
+
+def test_combine_beyond_2_31_elements(q4k):
+    t, top_k, hidden = 70001, 8, 4096
+    if torch.cuda.mem_get_info()[0] < 16e9:
+        pytest.skip("needs 16 GB of device memory")
+    z = torch.randn(t * top_k, hidden, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    assert z.numel() > 2 ** 31
+    ids = torch.zeros((t, top_k), dtype=torch.int32, device="cuda")
+    w = torch.rand((t, top_k), device="cuda", generator=torch.Generator(device="cuda").manual_seed(6))
+    y = torch.full((t, hidden), float("nan"), device="cuda")
+    q4k.q4k_moe_combine(z, ids, w, None, y, t, top_k, hidden)
+    at = 2 ** 31 // (hidden * top_k)
+    for rows in (slice(0, 3), slice(at - 2, at + 2), slice(t - 3, t)):
+        terms = z.view(t, top_k, hidden)[rows].double() * w[rows].double().unsqueeze(-1)
+        tol = top_k * 2.0 ** -24 * 1.0001 * terms.abs().sum(1) + 1e-37
+        assert bool(((y[rows].double() - terms.sum(1)).abs() <= tol).all())
+    assert not bool(torch.isnan(y).any())
+    del z, y
+    torch.cuda.empty_cache()
+
+
+def test_captured_products_at_once(q4k):
+    """Two captured graphs whose calls copy x into a workspace, replayed on two streams
+    at once, beside eager calls on a third: each has its own rows."""
+    problems = [base.Problem(300 + 50 * i, 4, 2, 500, 1024, 400 + i, mats=2, half=True) for i in range(3)]
+    want = [base.run_product(q4k, p) for p in problems]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    graphs = []
+    for p, y in zip(problems[:2], outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            base.run_product(q4k, p, y)
+            base.run_product(q4k, p, y)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(10):
+        for y in outs:
+            y.fill_(base.FILL)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+            base.run_product(q4k, problems[2], outs[2], stream=streams[2])
+        torch.cuda.synchronize()
+        for y, w in zip(outs, want):
+            assert torch.equal(y, w)
+
+
+def test_calls_of_several_threads(q4k):
+    """Host threads with a stream each."""
+    from concurrent.futures import ThreadPoolExecutor
+    problems = [base.Problem(40, 4, 2, 300, 1024, 410 + i, mats=1 + i % 2, half=i >= 2) for i in range(4)]
+    want = [base.run_product(q4k, p) for p in problems]
+    torch.cuda.synchronize()
+
+    def work(i):
+        s = torch.cuda.Stream()
+        outs = [torch.full_like(want[i], base.FILL) for _ in range(20)]
+        torch.cuda.synchronize()
+        for y in outs:
+            base.run_product(q4k, problems[i], y, stream=s)
+        s.synchronize()
+        return all(torch.equal(y, want[i]) for y in outs)
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(4)))
+
+
+def test_no_memory_for_the_workspace(q4k):
+    """A call whose copy of x no device holds (2^28 pairs of one row) is refused with
+    the allocation's error, and the calls after it are answered."""
+    if torch.cuda.mem_get_info()[0] < 8e9:
+        pytest.skip("needs 8 GB of device memory")
+    p = base.Problem(40, 4, 2, 300, 1024, 420, half=True)
+    want = base.run_product(q4k, p)
+    pairs, k = 2 ** 28, 2048
+    assert pairs * k * 2 > 1e12
+    w = device_weights(1, 1, k, 7)
+    x = torch.zeros((1, k), dtype=torch.float16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    order = torch.full((pairs,), -1, dtype=torch.int32, device="cuda")
+    y = torch.full((pairs, 1), base.FILL, device="cuda")
+    status = q4k.q4k_moe_gemm_f16_status(w, x, off, order, y, 1, pairs, pairs, 1, k)
+    assert status == q4k.Q4K_ERR_CUDA and q4k.q4k_last_cuda_error() == 2      # cudaErrorMemoryAllocation
+    assert torch.equal(base.run_product(q4k, p), want)
+    torch.cuda.synchronize()
+    assert bool((y == base.FILL).all())
