@@ -20,7 +20,7 @@ from .capi import (  # noqa: F401
     q4k_gemm_f16, q4k_gemm_f16_status, q4k_prefill_f16, q4k_prefill_f16_status,
     q4k_prefill_f16_noalloc, q4k_prefill_f16_noalloc_status, Q4K_ERR_CAPACITY,
     Q4K_PREFILL_NOALLOC_MAX_ELEMS, Q4K_FAULT_ROUTE_RANGE, Q4K_MOE_GEMV_MAX_K, Q4K_MOE_GEMV_MAX_PAIRS,
-    Q4K_MOE_MAX_EXPERTS,
+    Q4K_MOE_MAX_EXPERTS, Q4K_MOE_GEMM_SWIGLU_MAX_K,
     Q4K_MOE_MAX_TOP_K, Q4K_MOE_RENORM, q4k_moe_route, q4k_moe_route_status, q4k_moe_gemv,
     q4k_moe_gemv_status, q4k_moe_gemv_swiglu, q4k_moe_gemv_swiglu_status, q4k_moe_gemm_f16,
     q4k_moe_gemm_f16_status, q4k_moe_gemm_swiglu_f16, q4k_moe_gemm_swiglu_f16_status,

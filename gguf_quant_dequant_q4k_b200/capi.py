@@ -35,6 +35,7 @@ Q4K_MOE_MAX_EXPERTS = 256
 Q4K_MOE_MAX_TOP_K = 16
 Q4K_MOE_GEMV_MAX_PAIRS = 4096
 Q4K_MOE_GEMV_MAX_K = 43008
+Q4K_MOE_GEMM_SWIGLU_MAX_K = 16777216
 Q4K_MOE_RENORM = 0x1     # q4k_moe_route flag: weights sum to 1 over the chosen experts
 Q4K_KERNEL_WARP_ROWS = 1
 Q4K_KERNEL_STREAM = 2

@@ -430,7 +430,7 @@ int moe_gemm(const void* w, const void* w2, bool swiglu, const void* x, const in
              int n_experts, int n_pairs, int per_row, int n, int k, q4k_stream_t stream) {
     MoeGroups g;
     int st = check_moe_product(w, w2, swiglu, x, 2, offsets, order, y, swiglu ? 2 : 4, swiglu ? 16 : 4, n_experts,
-                               n_pairs, per_row, n, k, INT32_MAX, INT32_MAX, &g);
+                               n_pairs, per_row, n, k, swiglu ? Q4K_MOE_GEMM_SWIGLU_MAX_K : INT32_MAX, INT32_MAX, &g);
     if (st != Q4K_OK || n_pairs == 0) return st;
     DeviceInfo dev;
     st = current_device_info(&dev);

@@ -38,7 +38,9 @@
 //   decoding (785 cycles per step, issue slots 0.67; without the arithmetic of
 //   the decoding, to see the rest: 624).
 // * Waits are bounded; a role that gives up raises Q4K_FAULT_COPY_TIMEOUT and
-//   the CTA lets its copies and MMAs land before shared memory and TMEM go.
+//   the CTA lets its copies and MMAs land before shared memory and TMEM go. The
+//   longest wait in order is the SwiGLU epilogue's for a whole row, about 0.7 us per
+//   step of 128 elements: 0.1 s for the longest row accepted, of about 1 s.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_fp16.h>

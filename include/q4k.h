@@ -91,6 +91,7 @@ enum q4k_status {
 #define Q4K_MOE_MAX_TOP_K 16    /* q4k_moe_route / q4k_moe_combine: most choices */
 #define Q4K_MOE_GEMV_MAX_PAIRS 4096 /* q4k_moe_gemv*: most pairs per call         */
 #define Q4K_MOE_GEMV_MAX_K 43008 /* q4k_moe_gemv*: longest rows                  */
+#define Q4K_MOE_GEMM_SWIGLU_MAX_K 16777216 /* q4k_moe_gemm_swiglu_f16: longest rows */
 
 /*
  * y = W x for m vectors.
@@ -464,7 +465,9 @@ Q4K_API int q4k_prefill_f16_noalloc(const void *w_f16, const float *x, float *y,
  *        them. They cannot be checked before launch: an expert whose offsets
  *        do not ascend within 0..n_pairs, and a slot whose order entry lies
  *        outside 0..n_pairs-1, is skipped (its rows unwritten) and raises
- *        Q4K_FAULT_ROUTE_RANGE. Order entries must be distinct.
+ *        Q4K_FAULT_ROUTE_RANGE; the other experts are computed. Order entries
+ *        must be distinct; where offsets that fall back and rise again give two
+ *        experts one slot, its row is either's.
  * n_experts 1..Q4K_MOE_MAX_EXPERTS (more: Q4K_ERR_SHAPE), n_experts * N below
  * 2^31; n_pairs == 0 launches nothing. Outputs must not overlap inputs.
  */
@@ -537,6 +540,7 @@ Q4K_API int q4k_moe_gemm_f16(const void *w, const void *x_f16, const int *offset
  * u = x16[row(s)] * Wu16_e^T, rows in slot order, 16-byte aligned: the x_f16
  * of the down projection (pairs_per_row 0). g and u carry the q4k_gemm_f16
  * bound; the epilogue's f32 error is far below the one rounding to binary16.
+ * K up to Q4K_MOE_GEMM_SWIGLU_MAX_K (longer: Q4K_ERR_SHAPE).
  * Returns a q4k_status.
  */
 Q4K_API int q4k_moe_gemm_swiglu_f16(const void *w_gate, const void *w_up, const void *x_f16,

@@ -416,3 +416,15 @@ def test_no_memory_for_the_workspace(q4k):
     assert torch.equal(base.run_product(q4k, p), want)
     torch.cuda.synchronize()
     assert bool((y == base.FILL).all())
+
+
+def test_longest_row_of_the_gated_gemm(q4k):
+    """No wait gives up on the longest row that is accepted."""
+    n, k = 2, q4k.Q4K_MOE_GEMM_SWIGLU_MAX_K
+    w = device_weights(1, n, k, 8)
+    x = torch.zeros((1, k), dtype=torch.float16, device="cuda")
+    off, order = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1], [0]))
+    y = torch.full((1, n), base.FILL, dtype=torch.float16, device="cuda")
+    q4k.q4k_moe_gemm_swiglu_f16(w, w, x, off, order, y, 1, 1, 1, n, k)
+    torch.cuda.synchronize()
+    assert q4k.q4k_device_fault_flags() == 0 and bool((y == 0).all())
