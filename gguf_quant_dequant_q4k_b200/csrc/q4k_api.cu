@@ -51,6 +51,7 @@ size_t weight_bytes_checked(int n, int k) {
 
 int cuda_failure(cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
+    cudaGetLastError();   // reported here: the next call's check of its launch must not find it again
     return Q4K_ERR_CUDA;
 }
 

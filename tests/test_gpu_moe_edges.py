@@ -418,6 +418,24 @@ def test_no_memory_for_the_workspace(q4k):
     assert bool((y == base.FILL).all())
 
 
+def test_a_refused_allocation_is_not_the_next_call_s_error(q4k):
+    """The dense calls look for a launch error of their own; what an earlier call has
+    reported is not one."""
+    pairs, k = 2 ** 28, 2048
+    if torch.cuda.mem_get_info()[0] < 8e9:
+        pytest.skip("needs 8 GB of device memory")
+    w = device_weights(1, 2, k, 9)
+    x = torch.zeros((1, k), dtype=torch.float16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    order = torch.full((pairs,), -1, dtype=torch.int32, device="cuda")
+    y = torch.empty((pairs, 1), device="cuda")
+    out = torch.empty((2, k), device="cuda")
+    for _ in range(2):
+        assert q4k.q4k_moe_gemm_f16_status(w, x, off, order, y, 1, pairs, pairs, 1, k) == q4k.Q4K_ERR_CUDA
+        assert q4k.q4k_dequant_f32_status(w, out, 2, k) == q4k.Q4K_OK
+    torch.cuda.synchronize()
+
+
 def test_longest_row_of_the_gated_gemm(q4k):
     """No wait gives up on the longest row that is accepted."""
     n, k = 2, q4k.Q4K_MOE_GEMM_SWIGLU_MAX_K
