@@ -31,12 +31,13 @@
 //   fp16 and keeps D for the whole row.
 // * Measured (times are of calls back to back; the clock falls to about 1.5 GHz
 //   under the large cases): 2048 tokens, 8 experts, top 2: gate/up 14336 x 4096
-//   0.82-0.93 ms = 1030-1170 TFLOP/s (cuBLAS bf16, sustained: 1428), bound by
-//   the MMAs, 1088 cycles per step of about 910; down 4096 x 14336 0.49-0.56 ms,
-//   bound by the decoding and the drains of D. 777 tokens, 64 experts, top 4
-//   (about 48 slots each): gate/up 1536 x 2048 100 us, down 55 us, bound by the
-//   decoding (785 cycles per step, issue slots 0.67; without the arithmetic of
-//   the decoding, to see the rest: 624).
+//   0.83-0.94 ms = 1030-1160 TFLOP/s (cuBLAS bf16, sustained: 1428), bound by
+//   the MMAs, 1088 cycles per step of about 910; down 4096 x 14336 0.50-0.56 ms,
+//   bound by the drains of D, which the MMAs wait for, and by 6 tiles per pair
+//   where 5.2 are due. 777 tokens, 64 experts, top 4 (about 48 slots each): gate/up
+//   1536 x 2048 111-121 us, down 56-61 us, bound by the latency of each decode
+//   warp's chain, load - decode - store - wait - arrival (785 cycles per step, 624
+//   without its arithmetic, 390 for the MMAs alone; issue slots 0.68).
 // * Waits are bounded; a role that gives up raises Q4K_FAULT_COPY_TIMEOUT and
 //   the CTA lets its copies and MMAs land before shared memory and TMEM go. The
 //   longest wait in order is the SwiGLU epilogue's for a whole row, about 0.7 us per

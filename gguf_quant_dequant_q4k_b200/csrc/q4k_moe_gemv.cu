@@ -32,11 +32,12 @@
 //   round is up to kRoundUnits units and all pieces meet in the cluster's shared
 //   memory. Pieces are added in a fixed order.
 // * Bound and measured. One token, 8 experts, top 2: gate/up 14336 x 4096 33 us
-//   (4.0 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 21
-//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 50 us, down 29 us.
-//   Of the one-token call about 6 us are its start (planning, digits, the
-//   first boxes), the loop runs at 0.58 of the issue slots; with three or four
-//   vectors per group the issue slots set the pace.
+//   (4.0 TB/s; twice the rows take 24 us more, 5.5 TB/s), down 4096 x 14336 20
+//   us; 24 tokens, 64 experts, top 4: gate/up 1536 x 2048 49 us, down 28 us.
+//   Of the one-token call about 6 us are its start (planning, digits, the first
+//   boxes). No unit is full in the loop: issue slots 0.60 and 0.58 used, DRAM 4.0
+//   and 3.6 TB/s; warps wait on their own chain (wait 21-23 % of the stalls) and,
+//   with several groups, at the barriers around the one digit image.
 #include <cstdint>
 #include <cuda.h>
 #include <type_traits>
@@ -750,8 +751,12 @@ int launch_moe_gemv(const DeviceInfo& dev, const void* w, const void* w2, const 
     if (!make_gemv_map(&mw, w, rows, nsb) || !make_gemv_map(&mw2, swiglu ? w2 : w, rows, nsb))
         return cuda_failure(cudaErrorInvalidValue);
     // Groups of up to four vectors, or of two where an expert has one pair on
-    // average (the image is half as large). The smallest cluster whose CTAs'
-    // parts of K fit (groups of two if none does).
+    // average (the image is half as large). Measured, groups of two / of four, us,
+    // gate/up then down: 8 experts 14336 x 4096, 2 pairs 33/39, 20/27; 8 pairs 76/85,
+    // 44/49; 16 pairs 122/132, 71/77 (four vectors of K = 4096 need two CTAs). 64
+    // experts 1536 x 2048, 16 pairs 24/27, 15/16; 48 pairs 36/39, 21/23; 64 pairs
+    // 42/36, 24/22; 128 pairs 61/58, 33/33; 256 pairs 98/88, 51/46. The smallest
+    // cluster whose CTAs' parts of K fit (groups of two if none does).
     int csize = 1, cap = g.pairs <= g.experts ? 2 : kVMaxVec;
     while (csize < kVMaxCluster && (nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) csize *= 2;
     if ((nsb + csize - 1) / csize > v_max_sbs(cap, swiglu, csize == 1)) cap = 2;
