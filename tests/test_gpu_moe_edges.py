@@ -114,6 +114,23 @@ def test_experts_with_sound_offsets_survive_bad_ones(q4k, per_row, mats, half, b
     assert (y[skipped] == base.FILL).all()
 
 
+@pytest.mark.parametrize("mats", [1, 2])
+@pytest.mark.parametrize("tokens,experts,top_k,n,k", [(4096, 2, 1, 20, 256), (256, 256, 16, 17, 512), (2048, 5, 2, 33, 4096)])
+def test_gemv_of_the_most_pairs(q4k, tokens, experts, top_k, n, k, mats):
+    assert tokens * top_k == q4k.Q4K_MOE_GEMV_MAX_PAIRS
+    p = base.Problem(tokens, experts, top_k, n, k, 500 + tokens, pad=7, mats=mats)
+    base.check_product(p, base.run_product(q4k, p), f"{tokens} tokens {experts}x{n}x{k}")
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("mats", [1, 2])
+def test_one_row_for_all_pairs(q4k, mats, half):
+    """pairs_per_row beyond the pairs: x is one row."""
+    p = base.Problem(150, 3, 1, 70, 768, 510, mats=mats, half=half, per_row=1000)
+    assert p.dx.shape[0] == 1
+    base.check_product(p, base.run_product(q4k, p), "one row")
+
+
 # The 64-bit product on the device: every output of cases that are too large for the CPU oracle's loops.
 
 def reference64(q4k, p):
