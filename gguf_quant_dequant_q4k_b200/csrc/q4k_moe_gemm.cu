@@ -51,6 +51,7 @@
 #include "q4k_pair.cuh"
 #include "q4k_per_device.h"
 #include "q4k_superblock.cuh"
+#include "q4k_tensor_map.h"
 
 namespace q4k {
 
@@ -653,22 +654,6 @@ q4k_moe_gather_kernel(const uint4* x, uint4* __restrict__ out, const MoeGroups g
                 if (c0 + 32 * i < row16) dst[c0 + 32 * i] = v[i];
         }
     }
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = [] {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            ptr = nullptr;
-        return reinterpret_cast<EncodeTiledFn>(ptr);
-    }();
-    return fn;
 }
 
 // (byte of a superblock, superblock, row) of all experts' rows, boxes of one
